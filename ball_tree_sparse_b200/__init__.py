@@ -8,6 +8,7 @@ fallback: importing fails loudly when the compiled library is missing.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -59,6 +60,19 @@ _SIGS = {
     "bt_coarse_workspace_size": ([_i64, _i32, _i32, _i32, ctypes.c_int], _sz),
     "bt_coarse_ball_attention": ([_P, _P, _P, _P, _i64, _i64, _i32, _i32, _i32, ctypes.c_int, _i32, _P, _P, _sz,
                                   _P], ctypes.c_int),
+    "bt_ball_attention_backward": ([_P, _P, _P, _P, _P, _i64, _i64, _i32, _i32, _i32, ctypes.c_int, _P, _P, _P, _P],
+                                   ctypes.c_int),
+    "bt_rms_norm": ([_P, _P, _P, _i64, _i32, ctypes.c_float, ctypes.c_int, _P, _P, _P], ctypes.c_int),
+    "bt_rms_norm_i8": ([_P, _P, _P, _i64, _i32, ctypes.c_float, ctypes.c_int, _P, _P, _P, _P], ctypes.c_int),
+    "bt_quantize_i8": ([_P, _i64, _i32, ctypes.c_int, _P, _P, _P], ctypes.c_int),
+    "bt_rms_norm_backward_workspace_size": ([_i64, _i32], _sz),
+    "bt_rms_norm_backward": ([_P, _P, _P, _P, _i64, _i32, ctypes.c_float, ctypes.c_int, _P, _P, _P, _sz, _P],
+                             ctypes.c_int),
+    "bt_qkv_project_i8": ([_P, _P, _i64, _i32, _P, _P, _i32, _i32, ctypes.c_int, _P, _P, _i64, _P, _P, _P, _P],
+                          ctypes.c_int),
+    "bt_projected_i8_workspace_size": ([_i64, _i64, _i32, _i32, _i32, ctypes.c_int], _sz),
+    "bt_projected_ball_attention_i8": ([_P, _P, _P, ctypes.c_float, _P, _i64, _i64, _i32, _P, _P, _i32, _i32, _i32,
+                                        ctypes.c_int, _P, _P, _P, _sz, _P], ctypes.c_int),
 }
 
 
@@ -405,3 +419,242 @@ def bsa_forward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, perm: torch.T
                             _dptr(out),
                             _dptr(sel), _dptr(ws), ws.numel(), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Training and 8-bit serving.  These calls check shapes, types and devices here; what they allocate (outputs and
+# workspaces not given) belongs to the stream the work is enqueued on.
+# ---------------------------------------------------------------------------
+def _want(name: str, t, shape, dtype, device):
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _on(device, stream):
+    """Checks that `device` is the current CUDA device (kernels and streams belong to it) and returns the context
+    in which outputs and workspaces are allocated: that of `stream` where one is given."""
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, tensors are on {device}")
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _distinct(name: str, *tensors):
+    ptrs = [t.data_ptr() for t in tensors if t is not None and t.numel()]
+    if len(set(ptrs)) != len(ptrs):
+        raise ValueError(f"{name} may not share memory")
+
+
+def bt_ball_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, dO: torch.Tensor,
+                               perm: torch.Tensor | None, m: int, out=None, npad: int | None = None, stream=None):
+    """Gradients (dQ, dK, dV) of bt_ball_attention(Q, K, V, perm, m) for the gradient dO of its output; the
+    probabilities are recomputed.  All tensors [rows, H, d], fp32 or bf16, original row order.  Rows that no slot
+    names are not written: give zeroed tensors as `out` where there are such rows."""
+    rows, H, d = Q.shape
+    dt = _dt(Q)
+    for n, t in (("K", K), ("V", V), ("dO", dO)):
+        _want(n, t, Q.shape, Q.dtype, Q.device)
+    if perm is not None:
+        _want("perm", perm, (perm.numel(),), torch.int32, Q.device)
+    if npad is None:
+        npad = perm.numel() if perm is not None else rows
+    if perm is not None and npad > perm.numel():
+        raise ValueError(f"npad is {npad}, perm has {perm.numel()} slots")
+    with _on(Q.device, stream):
+        if out is None:
+            out = tuple(torch.empty(Q.shape, dtype=Q.dtype, device=Q.device) for _ in range(3))
+        dQ, dK, dV = out
+        for n, t in (("dQ", dQ), ("dK", dK), ("dV", dV)):
+            _want(n, t, Q.shape, Q.dtype, Q.device)
+        _distinct("gradients and inputs", dQ, dK, dV)
+        for t in (dQ, dK, dV):
+            for u in (Q, K, V, dO):
+                _distinct("gradients and inputs", t, u)
+        _check("bt_ball_attention_backward",
+               _lib.bt_ball_attention_backward(_dptr(Q), _dptr(K), _dptr(V), _dptr(dO), _dptr(perm), npad, rows, m, H,
+                                               d, dt, _dptr(dQ), _dptr(dK), _dptr(dV), _stream(stream)))
+    return dQ, dK, dV
+
+
+def _norm_inputs(X, weight, residual):
+    rows, C = X.shape
+    _want("residual", residual, X.shape, X.dtype, X.device)
+    _want("weight", weight, (C,), torch.float32, X.device)
+    return rows, C, _dt(X)
+
+
+def bt_rms_norm(X: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                eps: float = 1e-6, out: torch.Tensor | None = None, hout: torch.Tensor | None = None, stream=None):
+    """(Y, h): h = X + residual (X itself without one), Y = h * weight / sqrt(mean(h^2) + eps) by row.
+    X [rows, C] fp32 or bf16; weight float32 [C]."""
+    rows, C, dt = _norm_inputs(X, weight, residual)
+    if hout is not None and residual is None:
+        raise ValueError("hout is the sum with a residual: without one it is X")
+    with _on(X.device, stream):
+        if out is None:
+            out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        if residual is not None and hout is None:
+            hout = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        _want("out", out, X.shape, X.dtype, X.device)
+        _want("hout", hout, X.shape, X.dtype, X.device)
+        _distinct("out and hout", out, hout)
+        _check("bt_rms_norm", _lib.bt_rms_norm(_dptr(X), _dptr(residual), _dptr(weight), rows, C, eps, dt,
+                                               _dptr(hout), _dptr(out), _stream(stream)))
+    return out, (X if residual is None else hout)
+
+
+def bt_rms_norm_i8(X: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                   eps: float = 1e-6, out: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                   hout: torch.Tensor | None = None, stream=None):
+    """(Yq, scale, h): bt_rms_norm with its output in 8 bits, Y = Yq * scale[:, None] up to rounding."""
+    rows, C, dt = _norm_inputs(X, weight, residual)
+    if hout is not None and residual is None:
+        raise ValueError("hout is the sum with a residual: without one it is X")
+    with _on(X.device, stream):
+        if out is None:
+            out = torch.empty(X.shape, dtype=torch.int8, device=X.device)
+        if scale is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=X.device)
+        if residual is not None and hout is None:
+            hout = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        _want("out", out, X.shape, torch.int8, X.device)
+        _want("scale", scale, (rows,), torch.float32, X.device)
+        _want("hout", hout, X.shape, X.dtype, X.device)
+        _check("bt_rms_norm_i8", _lib.bt_rms_norm_i8(_dptr(X), _dptr(residual), _dptr(weight), rows, C, eps, dt,
+                                                     _dptr(hout), _dptr(out), _dptr(scale), _stream(stream)))
+    return out, scale, (X if residual is None else hout)
+
+
+def bt_quantize_i8(X: torch.Tensor, out: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+    """(Xq, scale): each row of X [rows, C] in 8 bits, X = Xq * scale[:, None] up to rounding."""
+    rows, C = X.shape
+    dt = _dt(X)
+    with _on(X.device, stream):
+        if out is None:
+            out = torch.empty(X.shape, dtype=torch.int8, device=X.device)
+        if scale is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=X.device)
+        _want("out", out, X.shape, torch.int8, X.device)
+        _want("scale", scale, (rows,), torch.float32, X.device)
+        _check("bt_quantize_i8", _lib.bt_quantize_i8(_dptr(X), rows, C, dt, _dptr(out), _dptr(scale), _stream(stream)))
+    return out, scale
+
+
+def bt_rms_norm_backward_workspace_size(rows: int, C: int) -> int:
+    return int(_lib.bt_rms_norm_backward_workspace_size(rows, C))
+
+
+def bt_rms_norm_backward(dY: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None = None,
+                         dH: torch.Tensor | None = None, eps: float = 1e-6, out: torch.Tensor | None = None,
+                         dw: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """(dX, dw): gradients of bt_rms_norm.  h is its input as stored (its second result), dY the gradient of Y and
+    dH, if any, that of h through the residual stream.  dX is the gradient of X and of the residual alike; dw
+    (float32 [C]) is None without a weight."""
+    rows, C = h.shape
+    dt = _dt(h)
+    _want("dY", dY, h.shape, h.dtype, h.device)
+    _want("dH", dH, h.shape, h.dtype, h.device)
+    _want("weight", weight, (C,), torch.float32, h.device)
+    with _on(h.device, stream):
+        if out is None:
+            out = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+        if weight is not None and dw is None:
+            dw = torch.empty(C, dtype=torch.float32, device=h.device)
+        if dw is not None and ws is None:
+            n = bt_rms_norm_backward_workspace_size(rows, C)
+            if n == 0:
+                raise BtsError("bt_rms_norm_backward_workspace_size", 7)
+            ws = torch.empty(n, dtype=torch.uint8, device=h.device)
+        _want("out", out, h.shape, h.dtype, h.device)
+        _want("dw", dw, (C,), torch.float32, h.device)
+        _distinct("dX and h", out, h)
+        _check("bt_rms_norm_backward",
+               _lib.bt_rms_norm_backward(_dptr(dY), _dptr(dH), _dptr(h), _dptr(weight), rows, C, eps, dt, _dptr(out),
+                                         _dptr(dw), _dptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    return out, dw
+
+
+def bt_qkv_project_i8(Xq: torch.Tensor, xs: torch.Tensor, Wq: torch.Tensor, ws: torch.Tensor, H: int, d: int,
+                      dtype: torch.dtype = torch.bfloat16, perm: torch.Tensor | None = None,
+                      inv: torch.Tensor | None = None, out=None, stream=None):
+    """Q, K, V = (Xq * xs[:, None]) (Wq * ws[:, None])^T from 8-bit integers: Xq int8 [rows, C], xs float32 [rows];
+    Wq int8 [3*H*d, C], ws float32 [3*H*d].  perm, inv and the layout of the results as for bt_qkv_project."""
+    rows, C = Xq.shape
+    dev = Xq.device
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("Q, K and V are float32 or bfloat16")
+    _want("Xq", Xq, (rows, C), torch.int8, dev)
+    _want("xs", xs, (rows,), torch.float32, dev)
+    _want("Wq", Wq, (3 * H * d, C), torch.int8, dev)
+    _want("ws", ws, (3 * H * d,), torch.float32, dev)
+    npad = perm.numel() if perm is not None else rows
+    if perm is not None:
+        _want("perm", perm, (npad,), torch.int32, dev)
+    with _on(dev, stream):
+        if perm is not None and inv is None:
+            inv = bt_invert_perm(perm, rows, stream=stream)
+        if perm is not None:
+            _want("inv", inv, (rows,), torch.int32, dev)
+        if out is None:
+            out = tuple(torch.empty((npad, H, d), dtype=dtype, device=dev) for _ in range(3))
+        Q, K, V = out
+        for n, t in (("Q", Q), ("K", K), ("V", V)):
+            _want(n, t, (npad, H, d), dtype, dev)
+        _distinct("Q, K and V", Q, K, V)
+        _check("bt_qkv_project_i8",
+               _lib.bt_qkv_project_i8(_dptr(Xq), _dptr(xs), rows, C, _dptr(Wq), _dptr(ws), H, d,
+                                      BT_F32 if dtype == torch.float32 else BT_BF16, _dptr(perm), _dptr(inv), npad,
+                                      _dptr(Q), _dptr(K), _dptr(V), _stream(stream)))
+    return Q, K, V
+
+
+def bt_projected_i8_workspace_size(npad: int, rows: int, C: int, H: int, d: int, dtype: torch.dtype) -> int:
+    return int(_lib.bt_projected_i8_workspace_size(npad, rows, C, H, d, BT_F32 if dtype == torch.float32 else BT_BF16))
+
+
+def bt_projected_ball_attention_i8(X: torch.Tensor, perm: torch.Tensor | None, Wq: torch.Tensor, ws: torch.Tensor,
+                                   m: int, H: int, d: int, weight: torch.Tensor | None = None,
+                                   residual: torch.Tensor | None = None, eps: float = 1e-6,
+                                   out: torch.Tensor | None = None, hout: torch.Tensor | None = None,
+                                   work: torch.Tensor | None = None, npad: int | None = None, stream=None):
+    """One pre-norm attention layer with an 8-bit projection: (O, h), with h = X + residual (X without one) and O
+    the ball attention of Q/K/V projected from the normed rows in 8 bits.  X [rows, C]; Wq int8 [3*H*d, C] and ws
+    float32 [3*H*d] from bt_quantize_i8; O [rows, H, d] in X's type, original row order."""
+    rows, C, dt = _norm_inputs(X, weight, residual)
+    dev = X.device
+    if hout is not None and residual is None:
+        raise ValueError("hout is the sum with a residual: without one it is X")
+    _want("Wq", Wq, (3 * H * d, C), torch.int8, dev)
+    _want("ws", ws, (3 * H * d,), torch.float32, dev)
+    if perm is not None:
+        _want("perm", perm, (perm.numel(),), torch.int32, dev)
+    if npad is None:
+        npad = perm.numel() if perm is not None else rows
+    if perm is not None and npad > perm.numel():
+        raise ValueError(f"npad is {npad}, perm has {perm.numel()} slots")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((rows, H, d), dtype=X.dtype, device=dev)
+        if residual is not None and hout is None:
+            hout = torch.empty(X.shape, dtype=X.dtype, device=dev)
+        if work is None:
+            n = bt_projected_i8_workspace_size(npad, rows, C, H, d, X.dtype)
+            if n == 0:
+                raise BtsError("bt_projected_i8_workspace_size", 1)
+            work = torch.empty(n, dtype=torch.uint8, device=dev)
+        _want("out", out, (rows, H, d), X.dtype, dev)
+        _want("hout", hout, X.shape, X.dtype, dev)
+        _check("bt_projected_ball_attention_i8",
+               _lib.bt_projected_ball_attention_i8(_dptr(X), _dptr(residual), _dptr(weight), eps, _dptr(perm), npad,
+                                                   rows, C, _dptr(Wq), _dptr(ws), m, H, d, dt, _dptr(hout),
+                                                   _dptr(out), _dptr(work), work.numel(), _stream(stream)))
+    return out, (X if residual is None else hout)

@@ -401,6 +401,123 @@ bt_status bt_coarse_ball_attention(const void *Q, const void *K, const void *V, 
                                    int64_t rows, int32_t m, int32_t H, int32_t d, bt_dtype dt, int32_t stride, void *O,
                                    void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * Backward pass of bt_ball_attention: the gradients dQ, dK and dV of a loss
+ * from the gradient dO of its output, with the probabilities recomputed from
+ * Q and K (neither O nor any statistics of the forward pass are needed).  For
+ * the real rows i, j of one ball and each head, with s = 1/sqrt(d) and
+ * p_ij = softmax_j(s Q_i . K_j):
+ *     dV_j = sum_i p_ij dO_i
+ *     dS_ij = p_ij (dO_i . V_j - sum_l p_il dO_i . V_l)
+ *     dQ_i = s sum_j dS_ij K_j,   dK_j = s sum_i dS_ij Q_i
+ *   Q, K, V, perm, npad, rows, m, H, d, dt  as for bt_ball_attention
+ *   dO           dt [rows, H, d]
+ *   dQ, dK, dV   dt [rows, H, d] out, original row order; rows no slot names
+ *                are left untouched.  They may not overlap the inputs, nor one
+ *                another.
+ * All seven tensors must be 16-byte aligned (BT_ERR_ARG); rows < 2^31 - 1 and
+ * npad < 2^31 (BT_ERR_UNSUPPORTED).  A perm entry >= rows is a dummy, recorded
+ * as BT_ERR_INTERNAL; one row must not be named by two slots.  Values that are
+ * not finite reach the gradients of their own ball and head alone.  Softmax,
+ * delta and all sums are in float; for BT_BF16 with m <= 128 (tcgen05 tensor
+ * cores) p and dS are rounded to bf16 as operands of the last three products.
+ * No workspace and no atomics: equal calls give equal bits, and calls may run
+ * at the same time.
+ */
+bt_status bt_ball_attention_backward(const void *Q, const void *K, const void *V, const void *dO, const int32_t *perm,
+                                     int64_t npad, int64_t rows, int32_t m, int32_t H, int32_t d, bt_dtype dt,
+                                     void *dQ, void *dK, void *dV, void *stream);
+
+/*
+ * Root-mean-square norm of the feature rows before a layer's projection, with
+ * the residual's addition:
+ *     h = x + r, rounded to dt as it is stored (h = x when R is NULL)
+ *     y = h * w / sqrt(mean_c(h_c^2) + eps)
+ *   X     dt [rows, C]
+ *   R     dt [rows, C] or NULL: the residual
+ *   w     float [C] or NULL (ones)
+ *   Hout  dt [rows, C] out, or NULL: h, the next residual stream; only with R
+ *         (BT_ERR_ARG otherwise).  May be X or R itself.
+ *   Y     dt [rows, C] out; may be X or R itself, but not Hout
+ *   1 <= C <= 8192 (BT_ERR_UNSUPPORTED above);  eps >= 0 and finite
+ * The sum of squares and the norm are in float.  rows = 0 is a no-op.
+ */
+bt_status bt_rms_norm(const void *X, const void *R, const float *w, int64_t rows, int32_t C, float eps, bt_dtype dt,
+                      void *Hout, void *Y, void *stream);
+
+/*
+ * bt_rms_norm with an output in 8 bits and a scale for each row, the operand
+ * of bt_qkv_project_i8:
+ *     scale = max_c |y_c| / 127,   Yq = y / scale, rounded to nearest even
+ * A row of zeros has scale 0; a row with a value that is not finite has scale
+ * NaN (and Yq = 0), so that its products are NaN.
+ *   Yq  int8 [rows, C] out;  scale  float [rows] out
+ */
+bt_status bt_rms_norm_i8(const void *X, const void *R, const float *w, int64_t rows, int32_t C, float eps, bt_dtype dt,
+                         void *Hout, int8_t *Yq, float *scale, void *stream);
+
+/*
+ * The quantisation of bt_rms_norm_i8 alone: Xq[r, :] = X[r, :] / scale[r],
+ * scale[r] = max_c |X[r, c]| / 127.  Rows are tokens (features) or output
+ * channels (a weight of the layout Wt [3*H*d, C]).
+ */
+bt_status bt_quantize_i8(const void *X, int64_t rows, int32_t C, bt_dtype dt, int8_t *Xq, float *scale, void *stream);
+
+/*
+ * Backward pass of bt_rms_norm.  With g = w dY and rs = 1/sqrt(mean(h^2)+eps):
+ *     dX = rs (g - h rs^2 mean_c(g_c h_c)) + dH,    dw = sum over rows of dY h rs
+ *   dY   dt [rows, C]: gradient of Y
+ *   dH   dt [rows, C] or NULL: gradient that reaches h through the residual
+ *        stream (Hout)
+ *   Hs   dt [rows, C]: h as bt_rms_norm stored it (X where there was no R)
+ *   dX   dt [rows, C] out: the gradient of h, and so of both x and r.  May be
+ *        dY or dH itself, not Hs.
+ *   dw   float [C] out, or NULL
+ *   ws   workspace of bt_rms_norm_backward_workspace_size(rows, C) bytes,
+ *        256-byte aligned (partial sums of dw); not needed when dw is NULL
+ * rows = 0 sets dw to zero.  Sums are in float, in a fixed order: equal calls
+ * give equal bits.
+ */
+size_t bt_rms_norm_backward_workspace_size(int64_t rows, int32_t C);
+
+bt_status bt_rms_norm_backward(const void *dY, const void *dH, const void *Hs, const float *w, int64_t rows, int32_t C,
+                               float eps, bt_dtype dt, void *dX, float *dw, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * bt_qkv_project on 8-bit integers with a scale for each token and for each
+ * output channel:
+ *   out[o(r), h, k] = xs[r] ws[j] sum_c Xq[r, c] Wq[j, c],  j = t*H*d + h*d + k
+ *   Xq   int8 [rows, C] and xs float [rows], as bt_rms_norm_i8 and
+ *        bt_quantize_i8 write them
+ *   Wq   int8 [3*H*d, C] and ws float [3*H*d] (bt_quantize_i8 of Wt)
+ *   dt   type of Q, K and V
+ *   perm, inv, npad, Q, K, V  as for bt_qkv_project (slot order with zero rows
+ *        in the dummy slots, or the original order when perm is NULL)
+ * The sum is exact (32-bit integers); the result is rounded to dt once.
+ * C <= 65536, 3*H*d <= 65535 (BT_ERR_UNSUPPORTED).
+ */
+bt_status bt_qkv_project_i8(const int8_t *Xq, const float *xs, int64_t rows, int32_t C, const int8_t *Wq,
+                            const float *ws, int32_t H, int32_t d, bt_dtype dt, const int32_t *perm,
+                            const int32_t *inv, int64_t npad, void *Q, void *K, void *V, void *stream);
+
+/*
+ * One pre-norm attention layer served in 8 bits: bt_rms_norm_i8 of X (+ R),
+ * bt_qkv_project_i8, ball attention.  The counterpart of
+ * bt_projected_ball_attention; arguments as for the calls it is made of, with
+ * gamma the norm's weight.  Hout [rows, C] is the residual stream (or NULL;
+ * only with R).  C <= 8192.
+ *   work  workspace of bt_projected_i8_workspace_size(npad, rows, C, H, d, dt)
+ *         bytes, 256-byte aligned (the 8-bit rows and scales, Q, K, V and the
+ *         inverse of perm)
+ * With perm, every row must be named by a slot, as in a tree over the rows.
+ */
+size_t bt_projected_i8_workspace_size(int64_t npad, int64_t rows, int32_t C, int32_t H, int32_t d, bt_dtype dt);
+
+bt_status bt_projected_ball_attention_i8(const void *X, const void *R, const float *gamma, float eps,
+                                         const int32_t *perm, int64_t npad, int64_t rows, int32_t C, const int8_t *Wq,
+                                         const float *ws, int32_t m, int32_t H, int32_t d, bt_dtype dt, void *Hout,
+                                         void *O, void *work, size_t work_bytes, void *stream);
+
 /* Same as bt_last_device_status (the name of an earlier version of this library). */
 bt_status bt_attention_device_status(void *stream);
 
