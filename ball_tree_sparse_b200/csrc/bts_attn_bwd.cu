@@ -291,22 +291,23 @@ __global__ void __launch_bounds__(BwdSimt<D, MP>::NT)
 //   warps 0-7   group 0, warps 8-15 group 1: a group works on one head of a tile at a time, two threads per query row
 //               (TMEM lane), 64 keys each;
 //   warps 16, 17  producers: load perm and gather the rows of Q, K, V and dO by TMA (tile::gather4, 128-byte pieces,
-//               128-byte swizzle) into a stage.
-// d = 32: the two groups take the two heads of a pair, whose 64 bytes of a row are one piece (an item: tile, pair);
-// two stages, one producer.  d = 64: every group has its own items (tile, head), one stage and a producer, so that one
-// group computes while the other one's rows arrive.
+//               128-byte swizzle) into a stage, whose two parts (Q and K; V and dO) fill and empty apart;
+//   warps 18, 19  one per group: issues its products, and for d = 32 stores its results while the group computes.
+// d = 32: the two groups take the two heads of a pair, whose 64 bytes of a row are one piece (an item: tile, pair), from
+// two stages.  d = 64: every group has its own items (tile, head), one stage and a producer, so that one group computes
+// while the other one's rows arrive.
 // Per head:
-//   S = Q K^T and dP = dO V^T           TMEM columns [0, 128) and [128, 256) of the group
-//   e = exp2(s - own max), sums of e and e dP over the thread's 64 keys, joined with the other half's through
-//   shared memory; P = e / sum as bf16 into the group's 32 KB of shared memory ([query][key], two blocks of 64 keys,
-//   128-byte swizzle); dS = P (dP - delta) as bf16 into TMEM over S
-//   dV = P^T dO                         A read transposed (MN-major); beside dS
-//   dQ = dS K                           A from TMEM; over dP
+//   S = Q K^T and dP = dO V^T           128 columns of TMEM each
+//   e = exp2(s - max) over S, sums of e and e dP, by groups of 32 keys; a row's two threads join them through shared
+//   memory; P = e / sum as bf16 into the group's 32 KB of shared memory ([query][key], two blocks of 64 keys, 128-byte
+//   swizzle); dS = P (dP - delta) as bf16 over dP
+//   dV = P^T dO                         A read transposed (MN-major)
+//   dQ = dS K                           A from TMEM
 //   dS to shared memory over P once dV is done
-//   dK = dS^T Q                         beside dQ
-// P and dS take turns in one buffer, because two would leave no room for the second stage.  While one group waits for
-// the tensor cores, the other one computes; dV is stored while dK is computed, and dQ and dK while the next item's S
-// and dP are.
+//   dK = dS^T Q
+// P and dS take turns in one buffer, because two would leave no room for the second stage.  e lies in TMEM and not in
+// registers, which 640 threads would spill (64 values each beside dP: the spills cost 10 to 40% of the time).  For d = 32
+// the next item's S is computed while this one's dS is written.
 // A key of another ball or a dummy has P = dS = 0.  Where a tile holds several balls, a value of one ball that is not
 // finite would still reach the others as 0 * value: a result that is not finite is therefore summed again over the
 // ball's own slots (`mend`).
@@ -320,10 +321,10 @@ struct BwdTc {
     static constexpr uint32_t PBUF = 2 * BLK;
     static constexpr uint32_t P_OFF = 2 * STAGE;
     static constexpr uint32_t BYTES = P_OFF + 2 * PBUF + 1024;
-    static constexpr int THREADS = 640;
-    // Registers of a thread: at launch, then of a group's threads and of a producer's (setmaxnreg).
-    static constexpr int REGS = 96, REGS_G = 112, REGS_P = 32;
-    static_assert(512 * REGS_G + 128 * REGS_P <= THREADS * REGS, "the split is of what the block was launched with");
+    static constexpr int GROUP = 256, THREADS = 640;
+    // TMEM columns of a group: S, then e; dP, then dS (bf16 pairs) in columns 0-31 and 64-95 of it.  The results lie beside
+    // dS, and dK over it; what does not fit there (d = 64) over e.
+    static constexpr uint32_t TMEM = 256, T_G = 128, T_K = T_G, T_V = D == 32 ? T_G + 32 : 0, T_Q = D == 32 ? T_G + 96 : 64;
 };
 
 __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16])
@@ -336,13 +337,6 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[1
                  : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 template <int N>
 __device__ __forceinline__ void tmem_ld_nowait(uint32_t taddr, uint32_t (&r)[N])
 {
@@ -350,19 +344,83 @@ __device__ __forceinline__ void tmem_ld_nowait(uint32_t taddr, uint32_t (&r)[N])
     else tmem_ld32_nowait(taddr, r);
 }
 
-// Barrier of one group's 256 threads.
-__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 256;" ::"r"(g + 1) : "memory"); }
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 16) {
+        uint32_t v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = r[i + j];
+        tmem_st16(taddr + i, v);
+    }
+}
 
-// The same, and whether `p` holds for any of them.
+// Products with operands given as address / 16 and the rest of the descriptor.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint64_t da, uint32_t b, uint64_t db, uint32_t idesc,
+                                       uint32_t acc)
+{
+    mma_bf16(d, da | (a & 0x3FFFu), db | (b & 0x3FFFu), idesc, acc);
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint64_t db, uint32_t idesc, uint32_t acc)
+{
+    mma_bf16_ts(d, a, db | (b & 0x3FFFu), idesc, acc);
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred a;\n\telect.sync _|a, 0xffffffff;\n\tselp.u32 %0, 1, 0, a;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Named barriers: 1 + g, group g and the warp that issues its products; 3 + g, group g; 5 + 4 g + w, the two warps of
+// 32 rows.
+template <int N>
+__device__ __forceinline__ void named_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory"); }
+__device__ __forceinline__ void group_sync(int g) { named_sync<256>(3 + g); }
+
+// One arrival for the warp.
+__device__ __forceinline__ void warp_arrive(uint32_t bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Barrier of group g, and whether `p` holds for any of its threads.
 __device__ __forceinline__ bool group_any(int g, bool p)
 {
     uint32_t r;
     asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %2, 0;\n\tbar.red.or.pred b, %1, 256, a;\n\t"
                  "selp.u32 %0, 1, 0, b;\n\t}"
                  : "=r"(r)
-                 : "r"(g + 1), "r"(uint32_t(p))
+                 : "r"(3 + g), "r"(uint32_t(p))
                  : "memory");
     return r != 0;
+}
+
+// Pairs of floats in one packed instruction (sm_100), each lane an IEEE operation.
+__device__ __forceinline__ void ffma2_acc(float &a0, float &a1, float x0, float x1, float y0, float y1)
+{
+    asm("{\n\t.reg .b64 a, x, y;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "fma.rn.f32x2 a, x, y, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
+}
+__device__ __forceinline__ void fmul2(float x0, float x1, float y0, float y1, float &z0, float &z1)
+{
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(z0), "=f"(z1)
+        : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
+}
+__device__ __forceinline__ void fadd2(float x0, float x1, float y0, float y1, float &z0, float &z1)
+{
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(z0), "=f"(z1)
+        : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
@@ -377,6 +435,23 @@ __device__ __forceinline__ uint32_t swz(int row, int col)
     return uint32_t(row * 128 + ((((col >> 3) ^ (row & 7)) << 4) | ((col & 7) << 1)));
 }
 
+// Chunk c (16 bytes) of row r of result n in a group's buffer of P and dS.  The 32 rows of a pair of warps lie in that
+// pair's part of the buffer (both blocks); the chunks are swizzled, so that neither writing a row per lane nor reading
+// whole rows meets a bank conflict.
+template <int D>
+__device__ __forceinline__ uint4 *place(const uint8_t *gp, int n, int r, int c)
+{
+    const int rr = r & 31;
+    const int o = D == 32 ? n * 2048 + rr * 64 + (((c + (rr >> 1)) & 3) << 4)
+                          : n * 4096 + rr * 128 + ((c ^ (rr & 7)) << 4);
+    return reinterpret_cast<uint4 *>(const_cast<uint8_t *>(gp) + (o >> 12) * BwdTc<D>::BLK + (r >> 5) * 4096 + (o & 4095));
+}
+
+__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
     k_ball_bwd_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -389,15 +464,21 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
     constexpr bool OWN = L::OWN;
     constexpr int HALF_D = D / 2;
     constexpr uint32_t SBO = 1024, SW128 = 2, MN_A = 1u << 15;
+    // descriptors but for the address, in units of 16 bytes
+    constexpr uint64_t DESC = (uint64_t(SBO >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(SW128) << 61) | (1u << 16);
+    constexpr uint64_t DESC_P = (uint64_t(SBO >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(SW128) << 61) | (uint64_t(L::BLK >> 4) << 16);
     constexpr uint32_t IDESC_S = idesc_bf16(128, false);        // S, dP
     constexpr uint32_t IDESC_Q = idesc_bf16(D, true);           // dQ: A as it lies in TMEM
     constexpr uint32_t IDESC_T = idesc_bf16(D, true) | MN_A;    // dV, dK: A transposed
     extern __shared__ __align__(1024) uint8_t dsm[];
-    __shared__ __align__(8) uint64_t sFull[2], sEmpty[2], sBarS[2], sBarG[2], sBarV[2], sBarO[2];
+    // of a stage's parts (Q and K; V and dO), and of a group
+    __shared__ __align__(8) uint64_t sFull[2][2], sEmpty[2][2], sBarS[2], sBarG[2], sBarV[2], sBarO[2], sBarP[2],
+        sBarD[2], sBarF[2];
     __shared__ int32_t sRows[2][128];
     __shared__ uint32_t sMask[2][4];  // real slots of the tile
     __shared__ int32_t sItem[2];      // -1: no more work
     __shared__ float sX[2][2][3][128];  // per group and half: a row's max, sum and sum of e dP
+    __shared__ int32_t sOut[2][128];  // d = 32: rows of the results in the buffer
     __shared__ uint32_t sTmem;
     __shared__ int sAbort[2];
 
@@ -413,13 +494,17 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
     }
     if (tid == 32) {
         for (int i = 0; i < 2; ++i) {
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&sFull[i])) : "memory");
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&sEmpty[i])), "r"(OWN ? 1 : 2)
-                         : "memory");
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&sBarS[i])) : "memory");
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&sBarG[i])) : "memory");
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&sBarV[i])) : "memory");
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&sBarO[i])) : "memory");
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&sFull[i][j], 1);
+                mbar_init(&sEmpty[i][j], OWN ? 1 : 2);  // d = 32: two groups empty a stage
+            }
+            mbar_init(&sBarS[i], 1);
+            mbar_init(&sBarG[i], 1);
+            mbar_init(&sBarV[i], 1);
+            mbar_init(&sBarO[i], 1);
+            mbar_init(&sBarP[i], 8);
+            mbar_init(&sBarD[i], 8);
+            mbar_init(&sBarF[i], 1);
             sAbort[i] = 0;
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -431,12 +516,128 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
     const uint32_t tmem = sTmem;
 
     if (warp >= 16) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::REGS_P));
-        // ---------------- producer: lane l has rows 4l .. 4l+3 of the tile ----------------
-        const int g = warp - 16;
-        if (g < (OWN ? 2 : 1)) {  // the other warps fill their warpgroup
-            constexpr int NS = OWN ? 1 : 2;  // stages of this producer
-            const int first = OWN ? 2 * int(blockIdx.x) + g : int(blockIdx.x);
+        if (warp >= 18) {
+            // ---------------- products of group g; d = 32: and the stores of its results ----------------
+            const int g = __shfl_sync(0xffffffffu, warp, 0) - 18;
+            const uint32_t tS = __shfl_sync(0xffffffffu, tmem, 0) + L::TMEM * g;
+            const uint32_t barS = smem_u32(&sBarS[g]), barG = smem_u32(&sBarG[g]), barV = smem_u32(&sBarV[g]),
+                           barO = smem_u32(&sBarO[g]);
+            // operand addresses / 16.  Descriptors are made where they are used: kept in registers, they would spill.
+            auto stage16 = [&](int st) {
+                uint32_t a = (base + st * L::STAGE + (OWN ? 0 : 64 * g)) >> 4;
+                asm volatile("" : "+r"(a));
+                return a;
+            };
+            auto wait = [&](uint64_t *bar, uint32_t par) {
+                if (!mbar_wait(smem_u32(bar), par, status)) sAbort[g] = 1;
+                __syncwarp();
+                tc_fence_after();
+            };
+            auto issue_s = [&](int st) {
+                const uint32_t s0 = stage16(st);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_ss(tS, s0 + 2 * kk, DESC, s0 + (L::TENSOR + 32 * kk) / 16, DESC, IDESC_S, kk > 0);
+                    mma_commit(barS);
+                }
+                __syncwarp();
+            };
+            int h = 0;  // head of the results that wait in the buffer
+            for (int it = 0;; ++it) {
+                const int st = OWN ? g : it & 1;
+                const uint32_t use = (OWN ? it : it >> 1) & 1;
+                if (OWN || it == 0) wait(&sFull[st][0], use);
+                named_sync<L::GROUP + 32>(1 + g);  // the last results are out of TMEM, and item `it` is there
+                tc_fence_after();
+                const int item = sItem[st];
+                const bool stop = sAbort[g] || item < 0;
+                if (!stop) {
+                    if (OWN || it == 0) issue_s(st);
+                    wait(&sFull[st][1], use);
+                    const uint32_t s0 = stage16(st);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_ss(tS + L::T_G, s0 + (3 * L::TENSOR + 32 * kk) / 16, DESC,
+                                   s0 + (2 * L::TENSOR + 32 * kk) / 16, DESC, IDESC_S, kk > 0);
+                        mma_commit(barG);
+                    }
+                    __syncwarp();
+                }
+                if constexpr (!OWN) {
+                    if (it > 0) {
+                        // 8 rows of 64 bytes at a time
+                        const int c = lane & 3;
+#pragma unroll 2
+                        for (int i = 0; i < 16; ++i) {
+                            const int r = i * 8 + (lane >> 2);
+                            const int32_t to = sOut[g][r];
+                            if (to >= 0 && h < H) {
+                                const uint8_t *gp = gbase + L::P_OFF + g * L::PBUF;
+                                const size_t o = (size_t(to) * H + h) * D + c * 8;
+                                *reinterpret_cast<uint4 *>(dV + o) = *place<D>(gp, 0, r, c);
+                                *reinterpret_cast<uint4 *>(dQ + o) = *place<D>(gp, 1, r, c);
+                                *reinterpret_cast<uint4 *>(dK + o) = *place<D>(gp, 2, r, c);
+                            }
+                        }
+                        warp_arrive(smem_u32(&sBarF[g]));  // the buffer is free
+                    }
+                    h = (item % HP) * 2 + g;
+                }
+                if (stop) break;
+                wait(&sBarP[g], it & 1);  // P in shared memory, dS in TMEM
+                {
+                    const uint32_t s0 = stage16(st);
+                    uint32_t p0 = (base + L::P_OFF + g * L::PBUF) >> 4;
+                    asm volatile("" : "+r"(p0));
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ss(tS + L::T_V, p0 + 128 * kk, DESC_P, s0 + (3 * L::TENSOR + 2048 * kk) / 16, DESC,
+                                   IDESC_T, kk > 0);
+                        mma_commit(barV);
+                        if (OWN && spt <= m) mma_commit(smem_u32(&sEmpty[st][1]));
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ts(tS + L::T_Q, tS + L::T_G + 64 * (kk >> 2) + 8 * (kk & 3), s0 + (L::TENSOR + 2048 * kk) / 16, DESC, IDESC_Q, kk > 0);
+                    }
+                    __syncwarp();
+                }
+                bool ahead = false;  // the next S is on its way: e is not needed any more
+                if (!OWN && __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sFull[st ^ 1][0]), ((it + 1) >> 1) & 1))) {
+                    ahead = true;
+                    if (sItem[st ^ 1] >= 0) issue_s(st ^ 1);
+                }
+                wait(&sBarD[g], it & 1);  // dS in shared memory
+                {
+                    const uint32_t s0 = stage16(st);
+                    uint32_t p0 = (base + L::P_OFF + g * L::PBUF) >> 4;
+                    asm volatile("" : "+r"(p0));
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ss(tS + L::T_K, p0 + 128 * kk, DESC_P, s0 + 128 * kk, DESC, IDESC_T, kk > 0);
+                        mma_commit(barO);
+                        if (spt <= m) {  // the stage is free once these products are done
+                            mma_commit(smem_u32(&sEmpty[st][0]));
+                            if (!OWN) mma_commit(smem_u32(&sEmpty[st][1]));
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!OWN && !ahead) {
+                    wait(&sFull[st ^ 1][0], ((it + 1) >> 1) & 1);
+                    if (!*static_cast<volatile int *>(&sAbort[g]) && sItem[st ^ 1] >= 0) issue_s(st ^ 1);
+                }
+            }
+        } else {
+            // ---------------- producer p: lane l has rows 4l .. 4l+3 of the tile ----------------
+            // d = 32: part p of the two stages (0: Q, K, and the tile's rows; 1: V, dO); d = 64: both parts of group p's
+            // stage, V and dO first, which are free first
+            const int p = warp - 16;
+            constexpr int NS = OWN ? 1 : 2;
+            const int first = OWN ? 2 * int(blockIdx.x) + p : int(blockIdx.x);
             const int step = (OWN ? 2 : 1) * int(gridDim.x);
             const int32_t oob = int32_t(rows);  // a row outside the tensor reads zeros
             auto load_rows = [&](int item, int32_t(&r)[4]) {
@@ -448,11 +649,15 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
                         r[i] = perm ? __ldg(perm + s0 + i) : int32_t(s0 + i);
                 }
             };
+            auto emptied = [&](int st, int part, int it) {
+                bool ok = it < NS || mbar_wait(smem_u32(&sEmpty[st][part]), ((it / NS) - 1) & 1, status);
+                return bool(__all_sync(0xffffffffu, ok));
+            };
             int item = first, it = 0;
             int32_t cur[4];
             load_rows(item, cur);
             bool ok = true;
-            for (; item < items && ok; item += step) {
+            for (; item < items; item += step) {
                 int32_t nxt[4];
                 load_rows(item + step, nxt);  // items + step < 2^31, checked by the host
                 bool live = false;
@@ -465,110 +670,83 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
                     live |= cur[i] >= 0;
                 }
                 if (__any_sync(0xffffffffu, live)) {  // a tile of dummies has no results
-                    const int st = OWN ? g : it & 1;
-                    const uint32_t full = smem_u32(&sFull[st]);
-                    if (it >= NS) ok = mbar_wait(smem_u32(&sEmpty[st]), ((it / NS) - 1) & 1, status);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    uint32_t nib = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        sRows[st][4 * lane + i] = cur[i];
-                        nib |= uint32_t(cur[i] >= 0) << i;
-                    }
-                    nib <<= 4 * (lane & 7);
-                    for (int o = 1; o < 8; o <<= 1) nib |= __shfl_xor_sync(0xffffffffu, nib, o);
-                    if ((lane & 7) == 0) sMask[st][lane >> 3] = nib;
-                    __syncwarp();
-                    if (lane == 0) {
-                        sItem[st] = item;
-                        // arrive (release): the rows, the mask and the item are there; then the bytes of the gathers
-                        mbar_expect_tx(full, L::STAGE);
-                    }
-                    __syncwarp();
+                    const int st = OWN ? p : it & 1;
                     const uint32_t dst = base + st * L::STAGE + lane * 4 * 128;
                     const int32_t col = (item % HP) * 64;
-                    int32_t r[4];
+                    if (OWN || p == 1) {
+                        ok = emptied(st, 1, it);
+                        if (!ok) break;
+                        const uint32_t full = smem_u32(&sFull[st][1]);
+                        if (lane == 0) mbar_expect_tx(full, 2 * L::TENSOR);
+                        __syncwarp();
+                        int32_t r[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) r[i] = cur[i] >= 0 ? cur[i] : oob;
-                    tma_gather4(dst + 0 * L::TENSOR, &tmQ, col, r[0], r[1], r[2], r[3], full);
-                    tma_gather4(dst + 1 * L::TENSOR, &tmK, col, r[0], r[1], r[2], r[3], full);
-                    tma_gather4(dst + 2 * L::TENSOR, &tmV, col, r[0], r[1], r[2], r[3], full);
-                    tma_gather4(dst + 3 * L::TENSOR, &tmG, col, r[0], r[1], r[2], r[3], full);
+                        for (int i = 0; i < 4; ++i) r[i] = cur[i] >= 0 ? cur[i] : oob;
+                        tma_gather4(dst + 3 * L::TENSOR, &tmG, col, r[0], r[1], r[2], r[3], full);
+                        tma_gather4(dst + 2 * L::TENSOR, &tmV, col, r[0], r[1], r[2], r[3], full);
+                    }
+                    if (OWN || p == 0) {
+                        ok = emptied(st, 0, it);
+                        if (!ok) break;
+                        const uint32_t full = smem_u32(&sFull[st][0]);
+                        uint32_t nib = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            sRows[st][4 * lane + i] = cur[i];
+                            nib |= uint32_t(cur[i] >= 0) << i;
+                        }
+                        nib <<= 4 * (lane & 7);
+                        for (int o = 1; o < 8; o <<= 1) nib |= __shfl_xor_sync(0xffffffffu, nib, o);
+                        if ((lane & 7) == 0) sMask[st][lane >> 3] = nib;
+                        if (lane == 0) sItem[st] = item;
+                        __syncwarp();
+                        // arrive (release): the rows, the mask and the item are there; then the bytes of the gathers
+                        if (lane == 0) mbar_expect_tx(full, 2 * L::TENSOR);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) cur[i] = cur[i] >= 0 ? cur[i] : oob;
+                        tma_gather4(dst + 0 * L::TENSOR, &tmQ, col, cur[0], cur[1], cur[2], cur[3], full);
+                        tma_gather4(dst + 1 * L::TENSOR, &tmK, col, cur[0], cur[1], cur[2], cur[3], full);
+                    }
                     ++it;
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
             }
             // the end, through the next free stage; then wait for the gathers in flight
-            const int st = OWN ? g : it & 1;
-            if (ok && it >= NS) ok = mbar_wait(smem_u32(&sEmpty[st]), ((it / NS) - 1) & 1, status);
-            if (lane == 0) {
-                if (ok) {
+            const int st = OWN ? p : it & 1;
+            if (ok && (OWN || p == 0)) {
+                ok = emptied(st, 0, it);
+                if (ok && lane == 0) {
                     sItem[st] = -1;
-                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sFull[st])) : "memory");
+                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sFull[st][0])) : "memory");
                 }
-                // (an emptied stage's last gathers have landed, and its barrier is a phase further)
-                for (int k = it - 1; k >= 0 && k >= it - NS + int(ok); --k)
-                    mbar_wait(smem_u32(&sFull[OWN ? g : k & 1]), (k / NS) & 1, status);
+            }
+            // (an emptied part's last gathers have landed, and its barrier is a phase further)
+            if (lane == 0) {
+                if (OWN || p == 1)
+                    for (int k = it - 1; k >= 0 && k >= it - NS; --k)
+                        mbar_wait(smem_u32(&sFull[OWN ? p : k & 1][1]), (k / NS) & 1, status);
+                if (OWN || p == 0)
+                    for (int k = it - 1; k >= 0 && k >= it - NS + int(ok); --k)
+                        mbar_wait(smem_u32(&sFull[OWN ? p : k & 1][0]), (k / NS) & 1, status);
             }
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::REGS_G));
         // ---------------- one head: query row (and key row) r, keys and columns of half `half` ----------------
         const int g = warp >> 3, half = (warp >> 2) & 1, r = tid & 127;
-        const bool issuer = (tid & 255) == 0;
         const bool multi = spt > m;  // several balls in a tile
-        const uint32_t tS = tmem + 256 * g, tG = tS + 128;
-        const uint32_t tD = tS, tV = tS + 64, tQ = tG, tK = tG + 64;  // dS as bf16 pairs, and the results
-        const uint32_t lb = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + L::TMEM * g + (uint32_t((warp & 3) * 32) << 16), tG = tS + L::T_G;
+        const uint32_t tV = tS + L::T_V, tQ = tS + L::T_Q, tK = tS + L::T_K;
         const uint32_t barS = smem_u32(&sBarS[g]), barG = smem_u32(&sBarG[g]), barV = smem_u32(&sBarV[g]),
                        barO = smem_u32(&sBarO[g]);
-        const uint32_t pbuf = base + L::P_OFF + g * L::PBUF;
-        const uint32_t goff = OWN ? 0 : 64 * g;  // the head's bytes within a piece
+        const int pair = 5 + g * 4 + (warp & 3);  // barrier of the two warps that share 32 rows
         uint8_t *gp = gbase + L::P_OFF + g * L::PBUF;
         uint8_t *prow = gp + half * L::BLK + r * 128;
         const int b0 = r / m * m, b1 = min(b0 + m, spt);  // slots of the row's ball within the tile
         bool ok = true;
 
-        // Waits for item `it`, then issues its S and dP; the same answer for the group's threads.
-        auto begin = [&](int it) -> bool {
-            const int st = OWN ? g : it & 1;
-            ok = ok && mbar_wait(smem_u32(&sFull[st]), (OWN ? it : it >> 1) & 1, status);
-            if (!ok) sAbort[g] = 1;
-            tc_fence_before();
-            group_sync(g);
-            tc_fence_after();
-            if (sAbort[g]) return false;
-            if (sItem[st] < 0) return false;
-            if (issuer) {
-                const uint32_t s0 = base + st * L::STAGE + goff;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16(tS, smem_desc_sw(s0 + 32 * kk, 16, SBO, SW128),
-                             smem_desc_sw(s0 + L::TENSOR + 32 * kk, 16, SBO, SW128), IDESC_S, kk > 0);
-                mma_commit(barS);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16(tG, smem_desc_sw(s0 + 3 * L::TENSOR + 32 * kk, 16, SBO, SW128),
-                             smem_desc_sw(s0 + 2 * L::TENSOR + 32 * kk, 16, SBO, SW128), IDESC_S, kk > 0);
-                mma_commit(barG);
-            }
-            return true;
-        };
-        auto store_row = [&](__nv_bfloat16 *T, const uint32_t(&v)[HALF_D], float f, int32_t to, int h) {
-            if (to < 0 || h >= H) return;
-            uint4 *p = reinterpret_cast<uint4 *>(T + (size_t(to) * H + h) * D + half * HALF_D);
-#pragma unroll
-            for (int i = 0; i < HALF_D / 8; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = pack_bf16(__uint_as_float(v[8 * i + 2 * e]) * f, __uint_as_float(v[8 * i + 2 * e + 1]) * f);
-                p[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        };
         auto bad = [&](const uint32_t(&v)[HALF_D]) {
             bool b = false;
 #pragma unroll
@@ -578,192 +756,223 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
         // sum over the ball's slots x of w(x) * tensor[x][column]; w: row r of the buffer, or its column r.  Only for
         // rows r < spt, whose balls lie within the tile.
         auto mend = [&](uint32_t(&v)[HALF_D], bool column, const uint8_t *tensor) {
-            float a[HALF_D];
 #pragma unroll
-            for (int c = 0; c < HALF_D; ++c) a[c] = 0.0f;
-            for (int x = b0; x < b1; ++x) {
-                const int q = column ? x : r, k = column ? r : x;
-                const float w = __bfloat162float(
-                    *reinterpret_cast<const __nv_bfloat16 *>(gp + (k >> 6) * L::BLK + swz(q, k & 63)));
+            for (int c0 = 0; c0 < HALF_D; c0 += 8) {
+                float a[8];
 #pragma unroll
-                for (int c = 0; c < HALF_D; ++c) {
-                    const int col = half * HALF_D + c + int(goff / 2);
-                    a[c] = fmaf(w, __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(tensor + swz(x, col))),
-                                a[c]);
+                for (int c = 0; c < 8; ++c) a[c] = 0.0f;
+#pragma unroll 1
+                for (int x = b0; x < b1; ++x) {
+                    const int q = column ? x : r, k = column ? r : x;
+                    const float w = __bfloat162float(
+                        *reinterpret_cast<const __nv_bfloat16 *>(gp + (k >> 6) * L::BLK + swz(q, k & 63)));
+                    const int col = half * HALF_D + c0 + (OWN ? 0 : 32 * g);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        a[c] = fmaf(w, __bfloat162float(
+                                           *reinterpret_cast<const __nv_bfloat16 *>(tensor + swz(x, col + c))), a[c]);
                 }
-            }
 #pragma unroll
-            for (int c = 0; c < HALF_D; ++c) v[c] = __float_as_uint(a[c]);
+                for (int c = 0; c < 8; ++c) v[c0 + c] = __float_as_uint(a[c]);
+            }
+        };
+        auto put = [&](int n, const uint32_t(&v)[HALF_D], float f) {
+#pragma unroll
+            for (int i = 0; i < HALF_D / 8; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = pack_bf16(__uint_as_float(v[8 * i + 2 * e]) * f, __uint_as_float(v[8 * i + 2 * e + 1]) * f);
+                *place<D>(gp, n, r, half * (HALF_D / 8) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        };
+        // d = 64: the warp stores 16 of the pair's rows
+        auto store = [&](int n, __nv_bfloat16 *T, int32_t row, int h) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int rr = half * 16 + i * 4 + (lane >> 3), c = lane & 7;
+                const int32_t to = __shfl_sync(0xffffffffu, row, rr);
+                if (to >= 0)
+                    *reinterpret_cast<uint4 *>(T + (size_t(to) * H + h) * D + c * 8) =
+                        *place<D>(gp, n, (r & 96) + rr, c);
+            }
         };
 
-        bool go = begin(0);
-        for (int it = 0; go; ++it) {
+        for (int it = 0;; ++it) {
             const int st = OWN ? g : it & 1;
             const uint32_t par = it & 1;
-            const uint32_t s0 = base + st * L::STAGE + goff;
             const uint8_t *gs0 = gbase + st * L::STAGE;
-            const int32_t row = sRows[st][r];
+            if (ok) ok = mbar_wait(smem_u32(&sFull[st][0]), (OWN ? it : it >> 1) & 1, status);
+            if (!ok) sAbort[g] = 1;
+            tc_fence_before();
+            named_sync<L::GROUP + 32>(1 + g);
             const int item = sItem[st];
-            const int h = OWN ? item % HP : (item % HP) * 2 + g;
-            uint32_t cm[2];  // keys of this thread's two groups of 32 that count
+            if (sAbort[g] || item < 0) break;
+            const int32_t row = sRows[st][r];
+            // the keys of this thread's two groups of 32 that count, and for the warp: bit c, some count in group c;
+            // bit 2 + c, all
+            uint32_t cm[2];
+            int some = 0, all = 0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int k0 = half * 64 + c * 32;
                 const int lo = max(b0 - k0, 0), hi = min(b1 - k0, 32);
                 const uint32_t in = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
                 cm[c] = row >= 0 ? in & sMask[st][half * 2 + c] : 0u;
+                some |= int(__any_sync(0xffffffffu, cm[c] != 0u)) << c;
+                all |= int(__all_sync(0xffffffffu, cm[c] == 0xffffffffu)) << c;
             }
-            float e[64];
-            float mx = -INFINITY;
-            ok = ok && mbar_wait(barS, par, status);
+            // e = exp2(s - max) over S, the maximum and the sums of e and e dP by groups of 32 keys
+            float mc[2], sc[2], lc[2];
+            if (ok) ok = mbar_wait(barS, par, status);
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                uint32_t v[32];
-                if (__any_sync(0xffffffffu, cm[c] != 0u)) {
-                    tmem_ld32_nowait(tS + lb + half * 64 + c * 32, v);
-                    tmem_wait_ld();
-                } else {
+                mc[c] = -INFINITY;
+                sc[c] = lc[c] = 0.0f;
+                if (!((some >> c) & 1)) continue;
+                uint32_t e[32], v[32];
+                tmem_ld32_nowait(tS + half * 64 + c * 32, e);
+                tmem_wait_ld();
+                float s1 = 0.0f, l1 = 0.0f;
+                if ((all >> c) & 1) {
+                    float m1 = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0u;
-                }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) e[c * 32 + j] = __uint_as_float(v[j]);
-                if (__all_sync(0xffffffffu, cm[c] == 0xffffffffu)) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) mx = fmax3(mx, e[c * 32 + j], e[c * 32 + j + 1]);
+                    for (int j = 0; j < 32; j += 4) {
+                        mc[c] = fmax3(mc[c], __uint_as_float(e[j]), __uint_as_float(e[j + 1]));
+                        m1 = fmax3(m1, __uint_as_float(e[j + 2]), __uint_as_float(e[j + 3]));
+                    }
+                    mc[c] = fmaxf(mc[c], m1);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if ((cm[c] >> j) & 1u) mx = fmaxf(mx, e[c * 32 + j]);
+                        if ((cm[c] >> j) & 1u) mc[c] = fmaxf(mc[c], __uint_as_float(e[j]));
                 }
-            }
-            const float mxs = mx == -INFINITY ? 0.0f : mx * sl2;
-            float sa = 0.0f, sb = 0.0f;
+                const float mxs = mc[c] == -INFINITY ? 0.0f : mc[c] * sl2;
+                if (c == 0 || !(some & 1)) {
+                    if (ok) ok = mbar_wait(barG, par, status);
+                    tc_fence_after();
+                }
+                tmem_ld32_nowait(tG + half * 64 + c * 32, v);
+                if ((all >> c) & 1) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if (__all_sync(0xffffffffu, cm[c] == 0xffffffffu)) {
-#pragma unroll
-                    for (int j = c * 32; j < c * 32 + 32; j += 2) {
+                    for (int j = 0; j < 32; j += 2) {
                         float p0, p1;
-                        ffma2_bcast(e[j], e[j + 1], sl2, -mxs, p0, p1);
-                        e[j] = ex2(p0);
-                        e[j + 1] = ex2(p1);
-                        fadd2_acc(sa, sb, e[j], e[j + 1]);
+                        ffma2_bcast(__uint_as_float(e[j]), __uint_as_float(e[j + 1]), sl2, -mxs, p0, p1);
+                        e[j] = __float_as_uint(ex2(p0));
+                        e[j + 1] = __float_as_uint(ex2(p1));
+                        fadd2_acc(sc[c], s1, __uint_as_float(e[j]), __uint_as_float(e[j + 1]));
                     }
-                } else if (__any_sync(0xffffffffu, cm[c] != 0u)) {
+                    tmem_st<32>(tS + half * 64 + c * 32, e);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float p = ex2(fmaf(e[c * 32 + j], sl2, -mxs));
-                        e[c * 32 + j] = (cm[c] >> j) & 1u ? p : 0.0f;
-                        sa += e[c * 32 + j];
-                    }
+                    for (int j = 0; j < 32; j += 2)
+                        ffma2_acc(lc[c], l1, __uint_as_float(e[j]), __uint_as_float(e[j + 1]), __uint_as_float(v[j]),
+                                  __uint_as_float(v[j + 1]));
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) e[c * 32 + j] = 0.0f;
-                }
-            }
-            ok = ok && mbar_wait(barG, par, status);
-            tc_fence_after();
-            float la = 0.0f, lc = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t cmc = cm[c >> 1] >> (16 * (c & 1));
-                if (__any_sync(0xffffffffu, cm[c >> 1] != 0u)) {
-                    uint32_t v[16];
-                    tmem_ld16_nowait(tG + lb + half * 64 + c * 16, v);
-                    tmem_wait_ld();
-                    if (__all_sync(0xffffffffu, cm[c >> 1] == 0xffffffffu)) {
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            la = fmaf(e[c * 16 + j], __uint_as_float(v[j]), la);
-                            lc = fmaf(e[c * 16 + j + 1], __uint_as_float(v[j + 1]), lc);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if ((cmc >> j) & 1u) la = fmaf(e[c * 16 + j], __uint_as_float(v[j]), la);
+                    for (int j = 0; j < 32; ++j) {
+                        const float p = ex2(fmaf(__uint_as_float(e[j]), sl2, -mxs));
+                        e[j] = (cm[c] >> j) & 1u ? __float_as_uint(p) : 0u;
+                        sc[c] += __uint_as_float(e[j]);
                     }
+                    tmem_st<32>(tS + half * 64 + c * 32, e);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if ((cm[c] >> j) & 1u) lc[c] = fmaf(__uint_as_float(e[j]), __uint_as_float(v[j]), lc[c]);
                 }
+                sc[c] += s1;
+                lc[c] += l1;
             }
-            sX[g][half][0][r] = mx;
-            sX[g][half][1][r] = sa + sb;
-            sX[g][half][2][r] = la + lc;
-            tc_fence_before();  // S is read: dS comes over it
-            group_sync(g);
-            tc_fence_after();
-            float fs, delta;  // P = e fs
+            if (ok) ok = mbar_wait(barG, par, status);  // a warp without keys: dS comes over dP
+            float fs[2], delta;  // P = e fs
             {
+                // sums over a part without keys count for nothing, whatever they hold
+                const float mx = fmaxf(mc[0], mc[1]);
+                float f[2], den = 0.0f, dl = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    f[c] = mc[c] == -INFINITY ? 0.0f : ex2((mc[c] - mx) * sl2);
+                    if (cm[c]) { den = fmaf(sc[c], f[c], den); dl = fmaf(lc[c], f[c], dl); }
+                }
+                sX[g][half][0][r] = mx;
+                sX[g][half][1][r] = den;
+                sX[g][half][2][r] = dl;
+                named_sync<64>(pair);
                 const float mo = sX[g][half ^ 1][0][r], so = sX[g][half ^ 1][1][r], lo = sX[g][half ^ 1][2][r];
                 const float M = fmaxf(mx, mo);
                 const float f0 = mx == -INFINITY ? 0.0f : ex2((mx - M) * sl2);
                 const float f1 = mo == -INFINITY ? 0.0f : ex2((mo - M) * sl2);
-                // a half without keys adds nothing, whatever its sums hold
-                float den = 0.0f, dl = 0.0f;
-                if (cm[0] | cm[1]) { den = (sa + sb) * f0; dl = (la + lc) * f0; }
+                den *= f0;
+                dl *= f0;
                 if (so != 0.0f) { den = fmaf(so, f1, den); dl = fmaf(lo, f1, dl); }
                 const float inv = row >= 0 ? 1.0f / den : 0.0f;
-                fs = f0 * inv;
+                fs[0] = f[0] * f0 * inv;
+                fs[1] = f[1] * f0 * inv;
                 delta = dl * inv;
             }
+            if (!OWN && it > 0 && ok) ok = mbar_wait(smem_u32(&sBarF[g]), (it - 1) & 1, status);  // results are stored
+            tmem_wait_st();
+            uint32_t ds[32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                uint32_t w[8], ds[8];
-                if (__any_sync(0xffffffffu, cm[c >> 1] != 0u)) {
-                    const uint32_t cmc = cm[c >> 1] >> (16 * (c & 1));
-                    uint32_t v[16];
-                    tmem_ld16_nowait(tG + lb + half * 64 + c * 16, v);
+                uint32_t w[8];
+                if ((some >> (c >> 1)) & 1) {
+                    uint32_t e[16], v[16];
+                    const float f = fs[c >> 1];
+                    tmem_ld16_nowait(tS + half * 64 + c * 16, e);
+                    tmem_ld16_nowait(tG + half * 64 + c * 16, v);
                     tmem_wait_ld();
-                    const bool all = __all_sync(0xffffffffu, cm[c >> 1] == 0xffffffffu);
+                    if ((all >> (c >> 1)) & 1) {
 #pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        float p0 = e[c * 16 + k] * fs, p1 = e[c * 16 + k + 1] * fs;
-                        float d0 = p0 * (__uint_as_float(v[k]) - delta), d1 = p1 * (__uint_as_float(v[k + 1]) - delta);
-                        if (!all) {
-                            const bool on0 = (cmc >> k) & 1u, on1 = (cmc >> (k + 1)) & 1u;
-                            p0 = on0 ? p0 : 0.0f;
-                            p1 = on1 ? p1 : 0.0f;
-                            d0 = on0 ? d0 : 0.0f;
-                            d1 = on1 ? d1 : 0.0f;
+                        for (int k = 0; k < 16; k += 2) {
+                            float p0, p1, d0, d1;
+                            fmul2(__uint_as_float(e[k]), __uint_as_float(e[k + 1]), f, f, p0, p1);
+                            fadd2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]), -delta, -delta, d0, d1);
+                            fmul2(p0, p1, d0, d1, d0, d1);
+                            w[k >> 1] = pack_bf16(p0, p1);
+                            ds[c * 8 + (k >> 1)] = pack_bf16(d0, d1);
                         }
-                        w[k >> 1] = pack_bf16(p0, p1);
-                        ds[k >> 1] = pack_bf16(d0, d1);
+                    } else {
+                        const uint32_t on = cm[c >> 1] >> (16 * (c & 1));
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2) {
+                            const bool o0 = (on >> k) & 1u, o1 = (on >> (k + 1)) & 1u;
+                            const float p0 = o0 ? __uint_as_float(e[k]) * f : 0.0f;
+                            const float p1 = o1 ? __uint_as_float(e[k + 1]) * f : 0.0f;
+                            w[k >> 1] = pack_bf16(p0, p1);
+                            ds[c * 8 + (k >> 1)] = pack_bf16(o0 ? p0 * (__uint_as_float(v[k]) - delta) : 0.0f,
+                                                             o1 ? p1 * (__uint_as_float(v[k + 1]) - delta) : 0.0f);
+                        }
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j] = ds[j] = 0u;
+                    for (int j = 0; j < 8; ++j) w[j] = ds[c * 8 + j] = 0u;
                 }
                 *reinterpret_cast<uint4 *>(prow + (((c * 2) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 *reinterpret_cast<uint4 *>(prow + (((c * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-                tmem_st8(tD + lb + half * 32 + c * 8, ds);
             }
+            tmem_st<32>(tG + half * 64, ds);
             tmem_wait_st();
             fence_async_smem();
             tc_fence_before();
-            group_sync(g);
+            warp_arrive(smem_u32(&sBarP[g]));
+            if (ok) ok = mbar_wait(barV, par, status);
             tc_fence_after();
-            if (issuer) {
-                if (ok)
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16(tV, smem_desc_sw(pbuf + kk * 2048, L::BLK, SBO, SW128),
-                                 smem_desc_sw(s0 + 3 * L::TENSOR + kk * 2048, 16, SBO, SW128), IDESC_T, kk > 0);
-                mma_commit(barV);
-                if (ok)
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ts(tQ, tD + 8 * kk, smem_desc_sw(s0 + L::TENSOR + kk * 2048, 16, SBO, SW128),
-                                    IDESC_Q, kk > 0);
-            }
-            ok = ok && mbar_wait(barV, par, status);
-            tc_fence_after();
-            uint32_t ds[32], ov[HALF_D];
-            tmem_ld32_nowait(tD + lb + half * 32, ds);
-            tmem_ld_nowait<HALF_D>(tV + lb + half * HALF_D, ov);
-            tmem_wait_ld();
-            if (multi && group_any(g, row >= 0 && bad(ov))) {
-                if (row >= 0 && bad(ov)) mend(ov, true, gs0 + 3 * L::TENSOR);
-                group_sync(g);
+            if (multi) {  // while P is still there
+                uint32_t ov[HALF_D];
+                tmem_ld_nowait<HALF_D>(tV + half * HALF_D, ov);
+                tmem_wait_ld();
+                if (group_any(g, row >= 0 && bad(ov))) {
+                    if (row >= 0 && bad(ov)) mend(ov, true, gs0 + 3 * L::TENSOR);
+                    tmem_st<HALF_D>(tV + half * HALF_D, ov);
+                    tmem_wait_st();
+                    fence_async_smem();  // dO is read: the next rows may come over it
+                    group_sync(g);
+                }
+                if (OWN && (tid & 255) == 0)
+                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sEmpty[st][1])) : "memory");
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -771,37 +980,46 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
                     make_uint4(ds[4 * j], ds[4 * j + 1], ds[4 * j + 2], ds[4 * j + 3]);
             fence_async_smem();
             tc_fence_before();
-            group_sync(g);
-            tc_fence_after();
-            if (issuer) {
-                if (ok)
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16(tK, smem_desc_sw(pbuf + kk * 2048, L::BLK, SBO, SW128),
-                                 smem_desc_sw(s0 + kk * 2048, 16, SBO, SW128), IDESC_T, kk > 0);
-                mma_commit(barO);
-                if (!multi) mma_commit(smem_u32(&sEmpty[st]));  // the stage is free once these products are done
-            }
-            if (ok) store_row(dV, ov, 1.0f, row, h);
-            ok = ok && mbar_wait(barO, par, status);
+            warp_arrive(smem_u32(&sBarD[g]));
+            if (ok) ok = mbar_wait(barO, par, status);
             tc_fence_after();
             uint32_t oq[HALF_D], ok_[HALF_D];
-            tmem_ld_nowait<HALF_D>(tQ + lb + half * HALF_D, oq);
-            tmem_ld_nowait<HALF_D>(tK + lb + half * HALF_D, ok_);
+            tmem_ld_nowait<HALF_D>(tQ + half * HALF_D, oq);
+            tmem_ld_nowait<HALF_D>(tK + half * HALF_D, ok_);
             tmem_wait_ld();
             if (multi) {
                 if (group_any(g, row >= 0 && (bad(oq) || bad(ok_)))) {
                     if (row >= 0 && bad(oq)) mend(oq, false, gs0 + L::TENSOR);
                     if (row >= 0 && bad(ok_)) mend(ok_, true, gs0);
+                    fence_async_smem();
                     group_sync(g);
                 }
-                if (issuer)
-                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sEmpty[st])) : "memory");
+                if ((tid & 255) == 0) {
+                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sEmpty[st][0])) : "memory");
+                    if (!OWN)
+                        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sEmpty[st][1]))
+                                     : "memory");
+                }
             }
+            // The results take the place of dS, whose products are done, and leave from there in whole rows
+            put(1, oq, scale);
+            tmem_ld_nowait<HALF_D>(tV + half * HALF_D, oq);
+            tmem_wait_ld();
+            put(0, oq, 1.0f);
             const int32_t to = ok ? row : -1;
-            go = begin(it + 1);  // S and dP of the next item while these rows are stored
-            store_row(dQ, oq, scale, to, h);
-            store_row(dK, ok_, scale, to, h);
+            if constexpr (!OWN) {
+                put(2, ok_, scale);
+                if (half == 0) sOut[g][r] = to;
+            } else {
+                const int h = item % HP;
+                named_sync<64>(pair);
+                store(0, dV, to, h);
+                store(1, dQ, to, h);
+                named_sync<64>(pair);
+                put(0, ok_, scale);
+                named_sync<64>(pair);
+                store(0, dK, to, h);
+            }
         }
     }
     tc_fence_before();
@@ -868,9 +1086,6 @@ bt_status launch_tc(const BwdArgs &a)
     const int sms = device_sms(&dev);
     if (sms == 0) return BT_ERR_CUDA;
     const bt_status s = setup_once(set[dev], [&]() -> bt_status {
-        cudaFuncAttributes at;
-        if (cudaFuncGetAttributes(&at, k_ball_bwd_tc<D>) != cudaSuccess) return BT_ERR_CUDA;
-        if (at.numRegs < L::REGS) return BT_ERR_INTERNAL;  // the register split would wait for registers for ever
         return cudaFuncSetAttribute(k_ball_bwd_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) ==
                        cudaSuccess
                    ? BT_OK
