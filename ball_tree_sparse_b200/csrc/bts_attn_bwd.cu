@@ -367,6 +367,18 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint6
     mma_bf16_ts(d, a, db | (b & 0x3FFFu), idesc, acc);
 }
 
+// Whether an mbarrier's phase is complete, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.b32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -605,7 +617,7 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
                     __syncwarp();
                 }
                 bool ahead = false;  // the next S is on its way: e is not needed any more
-                if (!OWN && __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sFull[st ^ 1][0]), ((it + 1) >> 1) & 1))) {
+                if (!OWN && __all_sync(0xffffffffu, mbar_test(smem_u32(&sFull[st ^ 1][0]), ((it + 1) >> 1) & 1))) {
                     ahead = true;
                     if (sItem[st ^ 1] >= 0) issue_s(st ^ 1);
                 }
