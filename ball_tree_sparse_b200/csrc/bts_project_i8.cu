@@ -7,8 +7,12 @@
 //
 //  - k_project_i8_few   few rows: a warp per output channel, which reads the channel's weights once for up to
 //                       eight rows.  Bound by the weights' bytes and by latency.
-//  - k_project_i8_tile  any row length or alignment, many rows: 64 x 64 tiles on the CUDA cores (dp4a).
+//  - k_project_i8_tc    many rows: tcgen05 tensor cores.
+//  - k_project_i8_tile  many rows whose results are no multiple of 16 bytes, or not aligned to them: 64 x 64 tiles on
+//                       the CUDA cores (dp4a).
 #include <cuda_bf16.h>
+
+#include <cstring>
 
 #include "bts_internal.cuh"
 #include "bts_tc.cuh"
@@ -206,6 +210,374 @@ __global__ void __launch_bounds__(256)
         zero_dummies(perm, npad, out, int64_t(blockIdx.x) * 8 + (tid >> 5), int64_t(gridDim.x) * 8);
 }
 
+// ---------------------------------------------------------------------------
+// Tensor cores (tcgen05.mma kind::i8, 32-bit integer sums in TMEM).  A CTA keeps to one chunk of BN output channels and
+// walks the 128-row tiles of X:
+//   warps 9-12  loaders.  TMA: one thread fetches 128 x 128-byte boxes (128-byte swizzle; rows and columns outside read
+//               zeros).  Otherwise (row lengths or addresses that no tensor map takes) the four warps copy 16 bytes a
+//               thread, put together from aligned words.
+//   warp 8      issues the products, two accumulators of BN columns;
+//   warps 0-7   two warps per 32 rows, each half of the columns: scale, round, pass through 4 KB of shared memory of
+//               the warp's own, and store 128-byte pieces of rows to the row's slot of Q, K or V.
+// W stays in shared memory where the chunk's rows fit (`keep`), else it is fetched with each block of X.
+// Bound by the stores: 65,536 x 256 -> 768 bf16 in tree order is 118 MB, 18 us.
+// ---------------------------------------------------------------------------
+struct I8Tile {
+    static constexpr int BM = 128, BK = 128, THREADS = 13 * 32;
+    static constexpr uint32_t XBLK = BM * BK;
+    static constexpr uint32_t OUT = 8 * 4096;                       // the epilogue's pieces
+    static constexpr uint32_t ROOM = 220 * 1024 - OUT - 1024;       // for W and the ring
+    static constexpr int RING = 6;                                  // stages, at most
+};
+
+__device__ __forceinline__ void mma_i8(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// 16 bytes of row `r` at column c (a multiple of 16) of the [n][C] bytes at M, zeros outside; no alignment needed.
+__device__ __forceinline__ uint4 bytes16(const int8_t *__restrict__ M, int64_t n, int C, int64_t r, int c)
+{
+    uint4 v = make_uint4(0, 0, 0, 0);
+    const int left = min(16, C - c);
+    if (r >= n || left <= 0) return v;
+    const int8_t *p = M + size_t(r) * C + c;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const uintptr_t end = reinterpret_cast<uintptr_t>(M) + size_t(n) * C;  // words past it are put together from bytes
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(a & ~uintptr_t(3));
+    const int sh = int(a & 3) * 8;
+    uint32_t x[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(w + i);
+        x[i] = 0;
+        if (at >= a + left) continue;
+        if (at >= reinterpret_cast<uintptr_t>(M) && at + 4 <= end) {
+            x[i] = __ldg(w + i);
+        } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (at + b >= a && at + b < a + left)
+                    x[i] |= uint32_t(uint8_t(__ldg(reinterpret_cast<const int8_t *>(at + b)))) << (8 * b);
+        }
+    }
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[i] = __funnelshift_r(x[i], x[i + 1], sh);
+        const int rest = left - 4 * i;  // bytes of this word inside the row
+        if (rest <= 0) y[i] = 0;
+        else if (rest < 4) y[i] &= (1u << (8 * rest)) - 1u;
+    }
+    return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+template <typename T, int BN, bool TMA>
+__global__ void __launch_bounds__(I8Tile::THREADS, 1)
+    k_project_i8_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                    const int8_t *__restrict__ X, const float *__restrict__ xs, int64_t rows, int C,
+                    const int8_t *__restrict__ W, const float *__restrict__ ws, int nout, QkvOut<T> out,
+                    const int32_t *__restrict__ perm, const int32_t *__restrict__ inv, int64_t npad, int64_t tiles,
+                    int nch, int stages, bool keep, uint32_t *status)
+{
+    using L = I8Tile;
+    constexpr uint32_t WBLK = BN * L::BK, SBO = 1024, SW128 = 2;
+    // S32 sums of S8 and S8, both K-major, M = 128
+    constexpr uint32_t IDESC = (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(BN >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+    constexpr uint32_t COLS = BN == 256 ? 512 : BN == 128 ? 256 : 128;  // two accumulators
+    extern __shared__ __align__(1024) uint8_t psm[];
+    __shared__ __align__(8) uint64_t sWFull, sFull[L::RING], sEmpty[L::RING], sAccFull[2], sAccEmpty[2];
+    __shared__ __align__(16) float sScale[BN];
+    __shared__ uint32_t sTmem;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int KB = (C + L::BK - 1) / L::BK;
+    const int chunk = int(blockIdx.x) % nch;
+    const int64_t groups = int64_t(gridDim.x) / nch, first = int64_t(blockIdx.x) / nch;
+    const uint32_t base = (smem_u32(psm) + 1023u) & ~1023u;
+    uint8_t *gbase = psm + (base - smem_u32(psm));
+    const uint32_t ring = L::OUT + (keep ? uint32_t(KB) * WBLK : 0);  // offsets from base: pieces, W, ring
+    const uint32_t stage = L::XBLK + (keep ? 0 : WBLK);
+    constexpr uint32_t LOADERS = TMA ? 1 : 4;
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sTmem)),
+                     "r"(COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 32) {
+        auto init = [](uint64_t *b, uint32_t n) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
+        };
+        init(&sWFull, LOADERS);
+        for (int i = 0; i < L::RING; ++i) {
+            init(&sFull[i], LOADERS);
+            init(&sEmpty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            init(&sAccFull[i], 1);
+            init(&sAccEmpty[i], 8);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    for (int j = tid; j < BN; j += L::THREADS) sScale[j] = chunk * BN + j < nout ? __ldg(ws + chunk * BN + j) : 0.0f;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sTmem;
+
+    if (warp >= 9) {
+        if (TMA) {
+            if (warp == 9 && lane == 0) {
+                bool ok = true;
+                if (keep) {
+                    mbar_expect_tx(smem_u32(&sWFull), uint32_t(KB) * WBLK);
+                    for (int k = 0; k < KB; ++k)
+                        tma_load_2d(base + L::OUT + k * WBLK, &tmW, k * L::BK, chunk * BN, smem_u32(&sWFull));
+                }
+                int i = 0;
+                for (int64_t tile = first; tile < tiles && ok; tile += groups)
+                    for (int k = 0; k < KB && ok; ++k, ++i) {
+                        const int s = i % stages;
+                        if (i >= stages) ok = mbar_wait(smem_u32(&sEmpty[s]), ((i / stages) - 1) & 1, status);
+                        if (ok) {
+                            const uint32_t full = smem_u32(&sFull[s]), at = base + ring + s * stage;
+                            mbar_expect_tx(full, stage);
+                            tma_load_2d(at, &tmX, k * L::BK, int32_t(tile * L::BM), full);
+                            if (!keep) tma_load_2d(at + L::XBLK, &tmW, k * L::BK, chunk * BN, full);
+                        }
+                    }
+                // the copies in flight
+                if (keep) mbar_wait(smem_u32(&sWFull), 0, status);
+                for (int k = i - 1; k >= 0 && k >= i - stages; --k)
+                    mbar_wait(smem_u32(&sFull[k % stages]), (k / stages) & 1, status);
+            }
+        } else {
+            const int lt = tid - 9 * 32;  // 0 .. 127
+            auto block = [&](const int8_t *M, int64_t n, int64_t r0, int nr, int k, uint32_t off) {
+#pragma unroll 4
+                for (int u = lt; u < nr * 8; u += 128) {
+                    const int r = u >> 3, c = u & 7;
+                    const uint4 v = bytes16(M, n, C, r0 + r, k * L::BK + c * 16);
+                    *reinterpret_cast<uint4 *>(gbase + off + r * 128 + ((c ^ (r & 7)) << 4)) = v;
+                }
+            };
+            auto arrive = [&](uint64_t *bar) {
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+            };
+            bool ok = true;
+            if (keep) {
+                for (int k = 0; k < KB; ++k) block(W, nout, chunk * BN, BN, k, L::OUT + k * WBLK);
+                arrive(&sWFull);
+            }
+            int i = 0;
+            for (int64_t tile = first; tile < tiles && ok; tile += groups)
+                for (int k = 0; k < KB && ok; ++k, ++i) {
+                    const int s = i % stages;
+                    if (i >= stages) ok = mbar_wait(smem_u32(&sEmpty[s]), ((i / stages) - 1) & 1, status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    block(X, rows, tile * L::BM, L::BM, k, ring + s * stage);
+                    if (!keep) block(W, nout, chunk * BN, BN, k, ring + s * stage + L::XBLK);
+                    arrive(&sFull[s]);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ---------------- products (one thread) ----------------
+        if (lane == 0) {
+            bool ok = !keep || mbar_wait(smem_u32(&sWFull), 0, status);
+            tc_fence_after();
+            int i = 0, ai = 0;
+            for (int64_t tile = first; tile < tiles && ok; tile += groups, ++ai) {
+                const int ab = ai & 1;
+                if (ai >= 2) ok = mbar_wait(smem_u32(&sAccEmpty[ab]), ((ai >> 1) - 1) & 1, status);
+                tc_fence_after();
+                const uint32_t acc = tmem + uint32_t(ab) * BN;
+                for (int k = 0; k < KB && ok; ++k, ++i) {
+                    const int s = i % stages;
+                    ok = mbar_wait(smem_u32(&sFull[s]), (i / stages) & 1, status);
+                    tc_fence_after();
+                    if (ok) {
+                        const uint32_t xa = base + ring + s * stage;
+                        const uint32_t wa = keep ? base + L::OUT + k * WBLK : xa + L::XBLK;
+                        const int nk = min(4, (C - k * L::BK + 31) / 32);  // zeros beyond the row length
+                        for (int kk = 0; kk < nk; ++kk)
+                            mma_i8(acc, smem_desc_sw(xa + 32 * kk, 16, SBO, SW128),
+                                   smem_desc_sw(wa + 32 * kk, 16, SBO, SW128), IDESC, (k | kk) != 0);
+                    }
+                    mma_commit(smem_u32(&sEmpty[s]));  // the stage is free once these products are done
+                }
+                mma_commit(smem_u32(&sAccFull[ab]));
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------- epilogue ----------------
+        constexpr int PC = 128 / int(sizeof(T));      // columns of a piece (128 bytes)
+        constexpr int CE = 16 / int(sizeof(T));       // columns of a chunk (16 bytes)
+        const int half = warp >> 2;
+        const uint32_t lb = uint32_t((warp & 3) * 32) << 16;
+        uint8_t *piece = gbase + warp * 4096;
+        bool ok = true;
+        int ai = 0;
+        for (int64_t tile = first; tile < tiles && ok; tile += groups, ++ai) {
+            const int64_t row = tile * L::BM + (warp & 3) * 32 + lane;
+            int32_t orow = -1;
+            float xr = 0.0f;
+            if (row < rows) {
+                xr = __ldg(xs + row);
+                orow = inv ? __ldg(inv + row) : int32_t(row);
+                if (inv && (orow < 0 || orow >= npad)) {  // not a slot: never write it
+                    if (half == 0 && chunk == 0) record_error(status, BT_ERR_INTERNAL);
+                    orow = -1;
+                }
+            }
+            const int ab = ai & 1;
+            ok = mbar_wait(smem_u32(&sAccFull[ab]), (ai >> 1) & 1, status);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            const uint32_t acc = tmem + uint32_t(ab) * BN + uint32_t(half * (BN / 2)) + lb;
+#pragma unroll 1
+            for (int c0 = 0; c0 < BN / 2; c0 += PC) {
+                const int jl = half * (BN / 2) + c0, j0 = chunk * BN + jl;
+                if (j0 >= nout || !ok) break;  // the same for every thread of the warp
+#pragma unroll
+                for (int q = 0; q < PC; q += 32) {
+                    if (c0 + q >= BN / 2) break;
+                    uint32_t v[32];
+                    tmem_ld32_nowait(acc + c0 + q, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int g = 0; g < 32; g += CE) {
+                        uint4 o;
+                        float f[CE];
+#pragma unroll
+                        for (int e = 0; e < CE; e += 4) {
+                            const float4 w = *reinterpret_cast<const float4 *>(sScale + jl + q + g + e);
+                            f[e] = float(int(v[g + e])) * xr * w.x;
+                            f[e + 1] = float(int(v[g + e + 1])) * xr * w.y;
+                            f[e + 2] = float(int(v[g + e + 2])) * xr * w.z;
+                            f[e + 3] = float(int(v[g + e + 3])) * xr * w.w;
+                        }
+                        if constexpr (sizeof(T) == 4) {
+                            o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                           __float_as_uint(f[3]));
+                        } else {
+                            uint32_t b[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+                                b[e] = *reinterpret_cast<const uint32_t *>(&t);
+                            }
+                            o = make_uint4(b[0], b[1], b[2], b[3]);
+                        }
+                        const int c = (q + g) / CE;  // chunk 0 .. 7 of the piece
+                        *reinterpret_cast<uint4 *>(piece + lane * 128 + ((c ^ (lane & 7)) << 4)) = o;
+                    }
+                }
+                __syncwarp();
+                // 4 rows of 128 bytes at a time
+                const int c = lane & 7, j = j0 + c * CE;
+                const bool in = c * CE < BN / 2 - c0 && j < nout;  // 3 H d is a multiple of a chunk
+                const int t = j / out.hd;
+                T *dst = (t == 0 ? out.q : t == 1 ? out.k : out.v) + (j - t * out.hd);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = i * 4 + (lane >> 3);
+                    const int32_t to = __shfl_sync(0xffffffffu, orow, r);
+                    const uint4 o = *reinterpret_cast<const uint4 *>(piece + r * 128 + ((c ^ (r & 7)) << 4));
+                    if (to >= 0 && in) *reinterpret_cast<uint4 *>(dst + size_t(to) * out.hd) = o;
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sAccEmpty[ab])) : "memory");
+        }
+        if (perm) zero_dummies(perm, npad, out, int64_t(blockIdx.x) * 8 + warp, int64_t(gridDim.x) * 8);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(COLS) : "memory");
+    }
+}
+
+template <typename T>
+struct I8Args {
+    const int8_t *X;
+    const float *xs;
+    int64_t rows;
+    int C;
+    const int8_t *W;
+    const float *ws;
+    int nout;
+    QkvOut<T> out;
+    const int32_t *perm, *inv;
+    int64_t npad;
+    bool tma;
+    int sms;
+    uint32_t *status;
+    cudaStream_t st;
+};
+
+template <typename T, int BN, bool TMA>
+bt_status run_project_tc(const I8Args<T> &a)
+{
+    using L = I8Tile;
+    static std::atomic<bool> set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return BT_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return BT_ERR_UNSUPPORTED;
+    const bt_status s = setup_once(set[dev], [&]() -> bt_status {
+        return cudaFuncSetAttribute(k_project_i8_tc<T, BN, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    int(L::ROOM + L::OUT + 1024)) == cudaSuccess
+                   ? BT_OK
+                   : BT_ERR_CUDA;
+    });
+    if (s != BT_OK) return s;
+    CUtensorMap mx, mw;
+    memset(&mx, 0, sizeof mx);
+    memset(&mw, 0, sizeof mw);
+    if (TMA && (!matrix_map(&mx, a.X, a.rows, a.C, 1, L::BK, L::BM) || !matrix_map(&mw, a.W, a.nout, a.C, 1, L::BK, BN)))
+        return BT_ERR_CUDA;
+    const int KB = (a.C + L::BK - 1) / L::BK;
+    const int64_t wbytes = int64_t(KB) * BN * L::BK;
+    const bool keep = wbytes + 3 * int64_t(L::XBLK) <= int64_t(L::ROOM);  // and three stages beside it
+    const uint32_t stage = L::XBLK + (keep ? 0 : BN * L::BK);
+    int stages = int((L::ROOM - (keep ? uint32_t(wbytes) : 0)) / stage);
+    if (stages > L::RING) stages = L::RING;
+    const size_t smem = L::OUT + 1024 + (keep ? size_t(wbytes) : 0) + size_t(stages) * stage;
+    const int nch = (a.nout + BN - 1) / BN;
+    const int64_t tiles = (a.rows + L::BM - 1) / L::BM;
+    int64_t groups = a.sms / nch;
+    if (groups < 1) groups = 1;
+    if (groups > tiles) groups = tiles;
+    k_project_i8_tc<T, BN, TMA><<<unsigned(groups * nch), L::THREADS, smem, a.st>>>(
+        mx, mw, a.X, a.xs, a.rows, a.C, a.W, a.ws, a.nout, a.out, a.perm, a.inv, a.npad, tiles, nch, stages, keep,
+        a.status);
+    return cudaPeekAtLastError() == cudaSuccess ? BT_OK : BT_ERR_CUDA;
+}
+
+template <typename T, bool TMA>
+bt_status launch_project_tc(const I8Args<T> &a)
+{
+    // wide chunks read X less often; narrow ones spread few rows over more SMs
+    const int64_t tiles = (a.rows + 127) / 128;
+    if (a.C <= 512 && tiles * ((a.nout + 255) / 256) >= a.sms) return run_project_tc<T, 256, TMA>(a);
+    if (tiles * ((a.nout + 127) / 128) >= a.sms) return run_project_tc<T, 128, TMA>(a);
+    return run_project_tc<T, 64, TMA>(a);
+}
+
 template <typename T>
 bt_status launch_project_i8(const int8_t *X, const float *xs, int64_t rows, int C, const int8_t *W, const float *ws,
                             int H, int d, const int32_t *perm, const int32_t *inv, int64_t npad, void *Q, void *K,
@@ -217,6 +589,15 @@ bt_status launch_project_i8(const int8_t *X, const float *xs, int64_t rows, int 
     const QkvOut<T> out{static_cast<T *>(Q), static_cast<T *>(K), static_cast<T *>(V), hd};
     const uintptr_t ali = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(W);
     const int lb = C % 16 == 0 && ali % 16 == 0 ? 16 : C % 4 == 0 && ali % 4 == 0 ? 4 : 1;
+    const uintptr_t alo = reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(K) |
+                          reinterpret_cast<uintptr_t>(V) | uintptr_t(hd * int(sizeof(T)));
+    if (rows > 4 * kFewRows && alo % 16 == 0) {
+        int dev = 0;
+        const int sms = device_sms(&dev);
+        if (sms == 0) return BT_ERR_CUDA;
+        const I8Args<T> a{X, xs, rows, C, W, ws, nout, out, perm, inv, npad, lb == 16, sms, status, st};
+        return lb == 16 ? launch_project_tc<T, true>(a) : launch_project_tc<T, false>(a);
+    }
     if (rows <= 4 * kFewRows) {
         const unsigned grid = unsigned((nout + kFewWarps - 1) / kFewWarps);
         auto kern = lb == 16 ? k_project_i8_few<T, 16> : lb == 4 ? k_project_i8_few<T, 4> : k_project_i8_few<T, 1>;
