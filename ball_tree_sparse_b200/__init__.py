@@ -8,7 +8,6 @@ fallback: importing fails loudly when the compiled library is missing.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -423,12 +422,20 @@ def bsa_forward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, perm: torch.T
 
 # ---------------------------------------------------------------------------
 # Training and 8-bit serving.  These calls check shapes, types and devices here; what they allocate (outputs and
-# workspaces not given) belongs to the stream the work is enqueued on.
+# workspaces not given) belongs to the stream the work is enqueued on.  A call's time on the host is what a small
+# problem costs, so the checks are kept to attribute comparisons.
 # ---------------------------------------------------------------------------
+# torch's own cheap look-ups of the current device and of its current stream's handle, where it has them
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _want(name: str, t, shape, dtype, device):
+    """Refuses a tensor of another shape, type or device."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
@@ -436,22 +443,61 @@ def _want(name: str, t, shape, dtype, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _on(device, stream):
-    """Checks that `device` is the current CUDA device (kernels and streams belong to it) and returns the context
-    in which outputs and workspaces are allocated: that of `stream` where one is given."""
+def _handle(device, stream):
+    """The handle of the stream to enqueue on (`stream`, or the current one), after a check that `device` is the current
+    CUDA device, which kernels and streams belong to."""
     if device.type != "cuda":
         raise ValueError("expected CUDA tensors")
-    if device.index != torch.cuda.current_device():
+    if device.index != _current_device():
         raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    if stream is not None and stream.device != device:
+    if stream is None:
+        return _current_stream(device.index)
+    if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, tensors are on {device}")
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return stream.cuda_stream
 
 
-def _distinct(name: str, *tensors):
-    ptrs = [t.data_ptr() for t in tensors if t is not None and t.numel()]
-    if len(set(ptrs)) != len(ptrs):
-        raise ValueError(f"{name} may not share memory")
+def _new(like: torch.Tensor, stream, shape=None, dtype=None):
+    """An uninitialised tensor on `like`'s device (of its shape and type where not given) that belongs to `stream`."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _new(like, None, shape, dtype)
+    if shape is None and dtype is None:
+        return torch.empty_like(like, requires_grad=False, memory_format=torch.contiguous_format)
+    return torch.empty(like.shape if shape is None else shape, dtype=dtype or like.dtype, device=like.device)
+
+
+def _at(t):
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _apart(name: str, t, *others, same=()):
+    """Refuses an output whose memory overlaps one of `others`, or a part of one of `same` (which it may be itself)."""
+    if t is None:
+        return
+    lo, hi = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+    for u, whole in [(u, False) for u in others] + [(u, True) for u in same]:
+        if u is None or u.numel() == 0 or lo == hi:
+            continue
+        a, b = u.data_ptr(), u.data_ptr() + u.numel() * u.element_size()
+        if lo < b and a < hi and not (whole and a == lo and b == hi):
+            raise ValueError(f"{name} may not share memory with another argument")
+
+
+def _slots(perm, npad, rows, device):
+    if perm is None:
+        return rows if npad is None else npad
+    n = perm.numel()
+    _want("perm", perm, (n,), torch.int32, device)
+    if npad is None:
+        return n
+    if npad > n:
+        raise ValueError(f"npad is {npad}, perm has {n} slots")
+    return npad
 
 
 def bt_ball_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, dO: torch.Tensor,
@@ -459,78 +505,88 @@ def bt_ball_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor
     """Gradients (dQ, dK, dV) of bt_ball_attention(Q, K, V, perm, m) for the gradient dO of its output; the
     probabilities are recomputed.  All tensors [rows, H, d], fp32 or bf16, original row order.  Rows that no slot
     names are not written: give zeroed tensors as `out` where there are such rows."""
-    rows, H, d = Q.shape
+    shape, dtype, dev = Q.shape, Q.dtype, Q.device
+    rows, H, d = shape
     dt = _dt(Q)
-    for n, t in (("K", K), ("V", V), ("dO", dO)):
-        _want(n, t, Q.shape, Q.dtype, Q.device)
-    if perm is not None:
-        _want("perm", perm, (perm.numel(),), torch.int32, Q.device)
-    if npad is None:
-        npad = perm.numel() if perm is not None else rows
-    if perm is not None and npad > perm.numel():
-        raise ValueError(f"npad is {npad}, perm has {perm.numel()} slots")
-    with _on(Q.device, stream):
-        if out is None:
-            out = tuple(torch.empty(Q.shape, dtype=Q.dtype, device=Q.device) for _ in range(3))
+    _want("K", K, shape, dtype, dev)
+    _want("V", V, shape, dtype, dev)
+    _want("dO", dO, shape, dtype, dev)
+    npad = _slots(perm, npad, rows, dev)
+    st = _handle(dev, stream)
+    if out is None:
+        dQ, dK, dV = _new(Q, stream), _new(Q, stream), _new(Q, stream)
+    else:
         dQ, dK, dV = out
         for n, t in (("dQ", dQ), ("dK", dK), ("dV", dV)):
-            _want(n, t, Q.shape, Q.dtype, Q.device)
-        _distinct("gradients and inputs", dQ, dK, dV)
-        for t in (dQ, dK, dV):
-            for u in (Q, K, V, dO):
-                _distinct("gradients and inputs", t, u)
-        _check("bt_ball_attention_backward",
-               _lib.bt_ball_attention_backward(_dptr(Q), _dptr(K), _dptr(V), _dptr(dO), _dptr(perm), npad, rows, m, H,
-                                               d, dt, _dptr(dQ), _dptr(dK), _dptr(dV), _stream(stream)))
+            _want(n, t, shape, dtype, dev)
+            _apart(n, t, Q, K, V, dO, perm, *(u for u in (dQ, dK, dV) if u is not t))
+        if dQ is dK or dQ is dV or dK is dV:
+            raise ValueError("dQ, dK and dV may not share memory")
+    _check("bt_ball_attention_backward",
+           _lib.bt_ball_attention_backward(_at(Q), _at(K), _at(V), _at(dO), _at(perm), npad, rows, m, H, d, dt, _at(dQ),
+                                           _at(dK), _at(dV), st))
     return dQ, dK, dV
 
 
-def _norm_inputs(X, weight, residual):
+def _norm_inputs(X, weight, residual, hout):
     rows, C = X.shape
+    dt = _dt(X)
     _want("residual", residual, X.shape, X.dtype, X.device)
-    _want("weight", weight, (C,), torch.float32, X.device)
-    return rows, C, _dt(X)
+    if weight is not None:
+        _want("weight", weight, (C,), torch.float32, X.device)
+    if hout is not None:
+        if residual is None:
+            raise ValueError("hout is the sum with a residual: without one it is X")
+        _want("hout", hout, X.shape, X.dtype, X.device)
+        _apart("hout", hout, weight, same=(X, residual))
+    return rows, C, dt
 
 
 def bt_rms_norm(X: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
                 eps: float = 1e-6, out: torch.Tensor | None = None, hout: torch.Tensor | None = None, stream=None):
     """(Y, h): h = X + residual (X itself without one), Y = h * weight / sqrt(mean(h^2) + eps) by row.
-    X [rows, C] fp32 or bf16; weight float32 [C]."""
-    rows, C, dt = _norm_inputs(X, weight, residual)
-    if hout is not None and residual is None:
-        raise ValueError("hout is the sum with a residual: without one it is X")
-    with _on(X.device, stream):
-        if out is None:
-            out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
-        if residual is not None and hout is None:
-            hout = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    X [rows, C] fp32 or bf16; weight float32 [C].  hout and out may be X or residual, but not one another."""
+    rows, C, dt = _norm_inputs(X, weight, residual, hout)
+    st = _handle(X.device, stream)
+    if out is None:
+        out = _new(X, stream)
+    else:
         _want("out", out, X.shape, X.dtype, X.device)
-        _want("hout", hout, X.shape, X.dtype, X.device)
-        _distinct("out and hout", out, hout)
-        _check("bt_rms_norm", _lib.bt_rms_norm(_dptr(X), _dptr(residual), _dptr(weight), rows, C, eps, dt,
-                                               _dptr(hout), _dptr(out), _stream(stream)))
+        _apart("out", out, weight, hout, same=(X, residual))
+    if residual is not None and hout is None:
+        hout = _new(X, stream)
+    _check("bt_rms_norm",
+           _lib.bt_rms_norm(_at(X), _at(residual), _at(weight), rows, C, eps, dt, _at(hout), _at(out), st))
     return out, (X if residual is None else hout)
+
+
+def _eight(X, out, scale, stream, others, same=()):
+    """The 8-bit rows and their scales, new ones where none are given."""
+    rows = X.shape[0]
+    if out is None:
+        out = _new(X, stream, dtype=torch.int8)
+    else:
+        _want("out", out, X.shape, torch.int8, X.device)
+        _apart("out", out, X, scale, *others)
+    if scale is None:
+        scale = _new(X, stream, (rows,), torch.float32)
+    else:
+        _want("scale", scale, (rows,), torch.float32, X.device)
+        _apart("scale", scale, X, *others)
+    return out, scale
 
 
 def bt_rms_norm_i8(X: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
                    eps: float = 1e-6, out: torch.Tensor | None = None, scale: torch.Tensor | None = None,
                    hout: torch.Tensor | None = None, stream=None):
     """(Yq, scale, h): bt_rms_norm with its output in 8 bits, Y = Yq * scale[:, None] up to rounding."""
-    rows, C, dt = _norm_inputs(X, weight, residual)
-    if hout is not None and residual is None:
-        raise ValueError("hout is the sum with a residual: without one it is X")
-    with _on(X.device, stream):
-        if out is None:
-            out = torch.empty(X.shape, dtype=torch.int8, device=X.device)
-        if scale is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=X.device)
-        if residual is not None and hout is None:
-            hout = torch.empty(X.shape, dtype=X.dtype, device=X.device)
-        _want("out", out, X.shape, torch.int8, X.device)
-        _want("scale", scale, (rows,), torch.float32, X.device)
-        _want("hout", hout, X.shape, X.dtype, X.device)
-        _check("bt_rms_norm_i8", _lib.bt_rms_norm_i8(_dptr(X), _dptr(residual), _dptr(weight), rows, C, eps, dt,
-                                                     _dptr(hout), _dptr(out), _dptr(scale), _stream(stream)))
+    rows, C, dt = _norm_inputs(X, weight, residual, hout)
+    st = _handle(X.device, stream)
+    out, scale = _eight(X, out, scale, stream, (weight, residual, hout))
+    if residual is not None and hout is None:
+        hout = _new(X, stream)
+    _check("bt_rms_norm_i8", _lib.bt_rms_norm_i8(_at(X), _at(residual), _at(weight), rows, C, eps, dt, _at(hout),
+                                                 _at(out), _at(scale), st))
     return out, scale, (X if residual is None else hout)
 
 
@@ -538,19 +594,14 @@ def bt_quantize_i8(X: torch.Tensor, out: torch.Tensor | None = None, scale: torc
     """(Xq, scale): each row of X [rows, C] in 8 bits, X = Xq * scale[:, None] up to rounding."""
     rows, C = X.shape
     dt = _dt(X)
-    with _on(X.device, stream):
-        if out is None:
-            out = torch.empty(X.shape, dtype=torch.int8, device=X.device)
-        if scale is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=X.device)
-        _want("out", out, X.shape, torch.int8, X.device)
-        _want("scale", scale, (rows,), torch.float32, X.device)
-        _check("bt_quantize_i8", _lib.bt_quantize_i8(_dptr(X), rows, C, dt, _dptr(out), _dptr(scale), _stream(stream)))
+    st = _handle(X.device, stream)
+    out, scale = _eight(X, out, scale, stream, ())
+    _check("bt_quantize_i8", _lib.bt_quantize_i8(_at(X), rows, C, dt, _at(out), _at(scale), st))
     return out, scale
 
 
 def bt_rms_norm_backward_workspace_size(rows: int, C: int) -> int:
-    return int(_lib.bt_rms_norm_backward_workspace_size(rows, C))
+    return _lib.bt_rms_norm_backward_workspace_size(rows, C)
 
 
 def bt_rms_norm_backward(dY: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None = None,
@@ -558,28 +609,39 @@ def bt_rms_norm_backward(dY: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
                          dw: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
     """(dX, dw): gradients of bt_rms_norm.  h is its input as stored (its second result), dY the gradient of Y and
     dH, if any, that of h through the residual stream.  dX is the gradient of X and of the residual alike; dw
-    (float32 [C]) is None without a weight."""
-    rows, C = h.shape
+    (float32 [C]) is None without a weight.  out may be dY or dH."""
+    shape, dtype, dev = h.shape, h.dtype, h.device
+    rows, C = shape
     dt = _dt(h)
-    _want("dY", dY, h.shape, h.dtype, h.device)
-    _want("dH", dH, h.shape, h.dtype, h.device)
-    _want("weight", weight, (C,), torch.float32, h.device)
-    with _on(h.device, stream):
-        if out is None:
-            out = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-        if weight is not None and dw is None:
-            dw = torch.empty(C, dtype=torch.float32, device=h.device)
-        if dw is not None and ws is None:
-            n = bt_rms_norm_backward_workspace_size(rows, C)
-            if n == 0:
-                raise BtsError("bt_rms_norm_backward_workspace_size", 7)
-            ws = torch.empty(n, dtype=torch.uint8, device=h.device)
-        _want("out", out, h.shape, h.dtype, h.device)
-        _want("dw", dw, (C,), torch.float32, h.device)
-        _distinct("dX and h", out, h)
-        _check("bt_rms_norm_backward",
-               _lib.bt_rms_norm_backward(_dptr(dY), _dptr(dH), _dptr(h), _dptr(weight), rows, C, eps, dt, _dptr(out),
-                                         _dptr(dw), _dptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    _want("dY", dY, shape, dtype, dev)
+    _want("dH", dH, shape, dtype, dev)
+    if weight is not None:
+        _want("weight", weight, (C,), torch.float32, dev)
+    st = _handle(dev, stream)
+    if dw is not None:
+        _want("dw", dw, (C,), torch.float32, dev)
+        _apart("dw", dw, h, weight, dY, dH, out)
+    elif weight is not None:
+        dw = _new(h, stream, (C,), torch.float32)
+    if out is not None:
+        _want("out", out, shape, dtype, dev)
+        _apart("out", out, h, weight, same=(dY, dH))
+    else:
+        out = _new(h, stream)
+    nb = 0
+    if ws is not None:
+        nb = ws.numel() * ws.element_size()
+        if ws.device != dev:
+            raise ValueError(f"ws is on {ws.device}, expected {dev}")
+        _apart("ws", ws, h, weight, dY, dH, out, dw)
+    elif dw is not None:
+        nb = _lib.bt_rms_norm_backward_workspace_size(rows, C)
+        if nb == 0:
+            raise BtsError("bt_rms_norm_backward_workspace_size", 7)
+        ws = _new(h, stream, (nb,), torch.uint8)
+    _check("bt_rms_norm_backward",
+           _lib.bt_rms_norm_backward(_at(dY), _at(dH), _at(h), _at(weight), rows, C, eps, dt, _at(out), _at(dw), _at(ws),
+                                     nb, st))
     return out, dw
 
 
@@ -592,33 +654,37 @@ def bt_qkv_project_i8(Xq: torch.Tensor, xs: torch.Tensor, Wq: torch.Tensor, ws: 
     dev = Xq.device
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("Q, K and V are float32 or bfloat16")
-    _want("Xq", Xq, (rows, C), torch.int8, dev)
+    _want("Xq", Xq, Xq.shape, torch.int8, dev)
     _want("xs", xs, (rows,), torch.float32, dev)
     _want("Wq", Wq, (3 * H * d, C), torch.int8, dev)
     _want("ws", ws, (3 * H * d,), torch.float32, dev)
-    npad = perm.numel() if perm is not None else rows
-    if perm is not None:
-        _want("perm", perm, (npad,), torch.int32, dev)
-    with _on(dev, stream):
-        if perm is not None and inv is None:
-            inv = bt_invert_perm(perm, rows, stream=stream)
-        if perm is not None:
-            _want("inv", inv, (rows,), torch.int32, dev)
-        if out is None:
-            out = tuple(torch.empty((npad, H, d), dtype=dtype, device=dev) for _ in range(3))
+    npad = _slots(perm, None, rows, dev)
+    st = _handle(dev, stream)
+    if perm is None:
+        inv = None
+    elif inv is None:
+        inv = bt_invert_perm(perm, rows, stream=stream)
+    else:
+        _want("inv", inv, (rows,), torch.int32, dev)
+    shape = (npad, H, d)
+    if out is None:
+        Q, K, V = _new(Xq, stream, shape, dtype), _new(Xq, stream, shape, dtype), _new(Xq, stream, shape, dtype)
+    else:
         Q, K, V = out
         for n, t in (("Q", Q), ("K", K), ("V", V)):
-            _want(n, t, (npad, H, d), dtype, dev)
-        _distinct("Q, K and V", Q, K, V)
-        _check("bt_qkv_project_i8",
-               _lib.bt_qkv_project_i8(_dptr(Xq), _dptr(xs), rows, C, _dptr(Wq), _dptr(ws), H, d,
-                                      BT_F32 if dtype == torch.float32 else BT_BF16, _dptr(perm), _dptr(inv), npad,
-                                      _dptr(Q), _dptr(K), _dptr(V), _stream(stream)))
+            _want(n, t, shape, dtype, dev)
+            _apart(n, t, Xq, xs, Wq, ws, perm, inv, *(u for u in (Q, K, V) if u is not t))
+        if Q is K or Q is V or K is V:
+            raise ValueError("Q, K and V may not share memory")
+    _check("bt_qkv_project_i8",
+           _lib.bt_qkv_project_i8(_at(Xq), _at(xs), rows, C, _at(Wq), _at(ws), H, d,
+                                  BT_F32 if dtype == torch.float32 else BT_BF16, _at(perm), _at(inv), npad, _at(Q),
+                                  _at(K), _at(V), st))
     return Q, K, V
 
 
 def bt_projected_i8_workspace_size(npad: int, rows: int, C: int, H: int, d: int, dtype: torch.dtype) -> int:
-    return int(_lib.bt_projected_i8_workspace_size(npad, rows, C, H, d, BT_F32 if dtype == torch.float32 else BT_BF16))
+    return _lib.bt_projected_i8_workspace_size(npad, rows, C, H, d, BT_F32 if dtype == torch.float32 else BT_BF16)
 
 
 def bt_projected_ball_attention_i8(X: torch.Tensor, perm: torch.Tensor | None, Wq: torch.Tensor, ws: torch.Tensor,
@@ -629,32 +695,30 @@ def bt_projected_ball_attention_i8(X: torch.Tensor, perm: torch.Tensor | None, W
     """One pre-norm attention layer with an 8-bit projection: (O, h), with h = X + residual (X without one) and O
     the ball attention of Q/K/V projected from the normed rows in 8 bits.  X [rows, C]; Wq int8 [3*H*d, C] and ws
     float32 [3*H*d] from bt_quantize_i8; O [rows, H, d] in X's type, original row order."""
-    rows, C, dt = _norm_inputs(X, weight, residual)
+    rows, C, dt = _norm_inputs(X, weight, residual, hout)
     dev = X.device
-    if hout is not None and residual is None:
-        raise ValueError("hout is the sum with a residual: without one it is X")
     _want("Wq", Wq, (3 * H * d, C), torch.int8, dev)
     _want("ws", ws, (3 * H * d,), torch.float32, dev)
-    if perm is not None:
-        _want("perm", perm, (perm.numel(),), torch.int32, dev)
-    if npad is None:
-        npad = perm.numel() if perm is not None else rows
-    if perm is not None and npad > perm.numel():
-        raise ValueError(f"npad is {npad}, perm has {perm.numel()} slots")
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((rows, H, d), dtype=X.dtype, device=dev)
-        if residual is not None and hout is None:
-            hout = torch.empty(X.shape, dtype=X.dtype, device=dev)
-        if work is None:
-            n = bt_projected_i8_workspace_size(npad, rows, C, H, d, X.dtype)
-            if n == 0:
-                raise BtsError("bt_projected_i8_workspace_size", 1)
-            work = torch.empty(n, dtype=torch.uint8, device=dev)
+    npad = _slots(perm, npad, rows, dev)
+    st = _handle(dev, stream)
+    if out is not None:
         _want("out", out, (rows, H, d), X.dtype, dev)
-        _want("hout", hout, X.shape, X.dtype, dev)
-        _check("bt_projected_ball_attention_i8",
-               _lib.bt_projected_ball_attention_i8(_dptr(X), _dptr(residual), _dptr(weight), eps, _dptr(perm), npad,
-                                                   rows, C, _dptr(Wq), _dptr(ws), m, H, d, dt, _dptr(hout),
-                                                   _dptr(out), _dptr(work), work.numel(), _stream(stream)))
+        _apart("out", out, X, residual, weight, Wq, ws, perm, hout, work)
+    else:
+        out = _new(X, stream, (rows, H, d), X.dtype)
+    if residual is not None and hout is None:
+        hout = _new(X, stream)
+    if work is None:
+        nb = bt_projected_i8_workspace_size(npad, rows, C, H, d, X.dtype)
+        if nb == 0:
+            raise BtsError("bt_projected_i8_workspace_size", 1)
+        work = _new(X, stream, (nb,), torch.uint8)
+    else:
+        nb = work.numel() * work.element_size()
+        if work.device != dev:
+            raise ValueError(f"work is on {work.device}, expected {dev}")
+        _apart("work", work, X, residual, weight, Wq, ws, perm, hout)
+    _check("bt_projected_ball_attention_i8",
+           _lib.bt_projected_ball_attention_i8(_at(X), _at(residual), _at(weight), eps, _at(perm), npad, rows, C, _at(Wq),
+                                               _at(ws), m, H, d, dt, _at(hout), _at(out), _at(work), nb, st))
     return out, (X if residual is None else hout)

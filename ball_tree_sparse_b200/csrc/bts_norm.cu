@@ -8,14 +8,18 @@
 //
 // Every kernel is bound by memory: a row is read once, held in registers between the reduction and the store, and
 // written once.  A row belongs to `tpr` threads (a power of two: part of a warp, a warp, or up to 8 warps), each
-// holding up to NV vectors of VEC elements, vector i of thread t at element (i * tpr + t) * VEC, so that neighbouring
-// threads read neighbouring bytes.  The vector is the widest that the row length and the pointers allow.
+// holding up to NV vectors of VEC elements (16 bytes), vector i of thread t the (i * tpr + t)-th of the row, so that
+// neighbouring threads read neighbouring bytes.
+// Vectors are aligned in memory, not in the row: where C is no multiple of VEC, row r begins `sh` = r C mod VEC elements
+// into its first vector, and the first and last vectors are read and written by element.  All tensors of a call have the
+// same shape, so they share the shift.  Only where an address is not aligned is VEC 1.
 #include <cuda_bf16.h>
 
 #include <cfloat>
 #include <cmath>
 
 #include "bts_internal.cuh"
+#include "bts_maps.cuh"
 
 namespace bts {
 namespace {
@@ -62,109 +66,156 @@ template <typename T> __device__ __forceinline__ T narrow(float v);
 template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// VEC floats of the weight, in 16-byte pieces where VEC allows
-template <int VEC>
-__device__ __forceinline__ void load_weight(const float *w, float (&f)[VEC])
+// The vectors of a row that a thread holds: vector i at column col(i) of C, `p` the row's first element; zeros where it has
+// none (or !live).  EDGE: the first and last may reach into the neighbouring rows, whose elements are read with the rest
+// (and perhaps while they are written) and dropped by mask_edge.  `end`: nothing follows the row, and single elements are
+// read where it ends inside a vector.  All loads are issued before any is used.
+template <bool EDGE, typename T, int VEC, int NV, typename F>
+__device__ __forceinline__ void load_row(Pack<T, VEC> (&k)[NV], const T *p, int C, bool live, bool end, F &&col)
 {
-    if constexpr (VEC >= 4) {
 #pragma unroll
-        for (int e = 0; e < VEC; e += 4) {
-            const float4 t = __ldg(reinterpret_cast<const float4 *>(w + e));
+    for (int i = 0; i < NV; ++i) {
+        const int c = col(i);
+        if (live && c < C && (!EDGE || (c + VEC > 0 && !(end && c + VEC > C)))) {
+            k[i] = load_pack<T, VEC>(p + c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) k[i].v[e] = T(0.0f);
+        }
+    }
+    if (EDGE && end && live) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = col(i);
+            if (c < C && c + VEC > C)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (c + e < C) k[i].v[e] = p[c + e];
+        }
+    }
+}
+
+template <bool EDGE, typename T, int VEC>
+__device__ __forceinline__ void mask_edge(Pack<T, VEC> &k, int c, int C)
+{
+    if constexpr (EDGE)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) k.v[e] = unsigned(c + e) < unsigned(C) ? k.v[e] : T(0.0f);
+}
+
+template <typename T, int VEC, bool EDGE>
+__device__ __forceinline__ void store_part(T *p, const Pack<T, VEC> &k, int c0, int C)
+{
+    if (!EDGE || (c0 >= 0 && c0 + VEC <= C)) {
+        store_pack<T, VEC>(p, k);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (unsigned(c0 + e) < unsigned(C)) p[e] = k.v[e];
+    }
+}
+
+// The weight's elements c0 ..: in 16-byte pieces where they are whole and aligned
+template <int VEC, bool EDGE>
+__device__ __forceinline__ void load_weight(const float *w, int c0, int C, float (&f)[VEC])
+{
+    if constexpr (VEC >= 4 && !EDGE) {
+#pragma unroll
+        for (int e = 0; e + 3 < VEC; e += 4) {
+            const float4 t = __ldg(reinterpret_cast<const float4 *>(w + c0 + e));
             f[e] = t.x; f[e + 1] = t.y; f[e + 2] = t.z; f[e + 3] = t.w;
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) f[e] = __ldg(w + e);
+        for (int e = 0; e < VEC; ++e) f[e] = !EDGE || unsigned(c0 + e) < unsigned(C) ? __ldg(w + c0 + e) : 0.0f;
     }
 }
 
-// Reduction over the tpr threads of a row; every thread gets the result.  The order of the additions depends on
-// tpr alone.  tpr > 32: `red` holds one value per warp, and the whole block (one row) calls it together.
-template <bool MAX>
-__device__ __forceinline__ float row_reduce(float v, int tpr, float *red)
+// Reductions over the tpr threads of a row; every thread gets the result.  The order of the additions depends on tpr
+// alone.  tpr > 32: `red` holds one value per warp of the block, the row's warps meet at a barrier of their own, and a
+// value stays until the row's next reduction but one (two halves, `turn`).
+__device__ __forceinline__ void row_barrier(int grp, int tpr)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(tpr) : "memory");
+}
+
+template <typename V, typename F>
+__device__ __forceinline__ V row_reduce(V v, int tpr, V *red, int &turn, F &&join)
 {
     const int o0 = tpr < 32 ? tpr : 32;
     for (int o = o0 >> 1; o > 0; o >>= 1) {
-        const float u = __shfl_xor_sync(0xffffffffu, v, o);
-        v = MAX ? fmaxf(v, u) : v + u;
+        V u;
+        if constexpr (sizeof(V) == 8) {
+            u.x = __shfl_xor_sync(0xffffffffu, v.x, o);
+            u.y = __shfl_xor_sync(0xffffffffu, v.y, o);
+        } else {
+            u = __shfl_xor_sync(0xffffffffu, v, o);
+        }
+        v = join(v, u);
     }
     if (tpr > 32) {
-        const int nw = tpr >> 5, lane = threadIdx.x & 31;
-        __syncthreads();  // the previous reduction's values are read
-        if (lane == 0) red[threadIdx.x >> 5] = v;
-        __syncthreads();
-        v = lane < nw ? red[lane] : 0.0f;  // maxima are of absolute values
-        for (int o = nw >> 1; o > 0; o >>= 1) {
-            const float u = __shfl_xor_sync(0xffffffffu, v, o);
-            v = MAX ? fmaxf(v, u) : v + u;
-        }
-        v = __shfl_sync(0xffffffffu, v, 0);
+        const int nw = tpr >> 5, w = threadIdx.x >> 5, w0 = w & ~(nw - 1);
+        V *half = red + 8 * (turn & 1);
+        ++turn;
+        if ((threadIdx.x & 31) == 0) half[w] = v;
+        row_barrier(w0 / nw, tpr);
+        v = half[w0];
+        for (int i = 1; i < nw; ++i) v = join(v, half[w0 + i]);
     }
     return v;
 }
 
 // One row per group of tpr threads.  I8: q and scale instead of Y.  norm == false: y = h (quantisation alone).
 // X, R and Hout may be the same tensor: a thread reads its elements before it writes them, so these loads are
-// plain ones.
-template <typename T, int VEC, int NV, bool I8>
+// plain ones.  SHIFT: C is no multiple of VEC.
+template <typename T, int VEC, int NV, bool SHIFT, bool I8>
 __global__ void __launch_bounds__(kNormThreads)
-    k_rms_norm(const T *X, const T *R, const float *__restrict__ w, int64_t rows, int C, int tpr, float eps,
-                           bool norm, T *Hout, T *Y, int8_t *Q, float *scale)
+    k_rms_norm(const T *X, const T *R, const float *__restrict__ w, int64_t rows, int C, float invC, int tpr,
+               float eps, bool norm, T *Hout, T *Y, int8_t *Q, float *scale)
 {
-    __shared__ float red[32];
+    __shared__ float red[16];
+    __shared__ uint32_t redm[16];
+    int turn = 0;
     const int rpb = int(blockDim.x) / tpr, t = int(threadIdx.x) % tpr;
     const int64_t row = int64_t(blockIdx.x) * rpb + int(threadIdx.x) / tpr;
     const bool live = row < rows;  // dead groups stay for the shuffles
     const size_t base = live ? size_t(row) * C : 0;
+    const int sh = SHIFT ? int(base & (VEC - 1)) : 0;
+    auto col = [&](int i) { return (i * tpr + t) * VEC - sh; };  // first column of vector i; below 0 in the row before
+    auto has = [&](int c) { return live && c < C && (!SHIFT || c + VEC > 0); };
 
     float h[NV * VEC];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + t) * VEC;
-        Pack<T, VEC> k;
-        if (live && c < C) {
-            k = load_pack<T, VEC>(X + base + c);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) h[i * VEC + e] = widen(k.v[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) h[i * VEC + e] = 0.0f;
-        }
-    }
-    if (R) {
-        Pack<T, VEC> rr[NV];
+    {
+        Pack<T, VEC> k[NV], rr[NV];
+        load_row<SHIFT>(k, X + base, C, live, row == rows - 1, col);
+        if (R) load_row<SHIFT>(rr, R + base, C, live, row == rows - 1, col);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
-            if (live && c < C) rr[i] = load_pack<T, VEC>(R + base + c);
-        }
+            const int c = col(i);
+            mask_edge<SHIFT>(k[i], c, C);
+            if (R) {
+                mask_edge<SHIFT>(rr[i], c, C);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
-            if (live && c < C) {
-                Pack<T, VEC> k;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    k.v[e] = narrow<T>(h[i * VEC + e] + widen(rr[i].v[e]));
-                    h[i * VEC + e] = widen(k.v[e]);
-                }
-                if (Hout) store_pack<T, VEC>(Hout + base + c, k);
+                for (int e = 0; e < VEC; ++e) k[i].v[e] = narrow<T>(widen(k[i].v[e]) + widen(rr[i].v[e]));
+                if (Hout && has(c)) store_part<T, VEC, SHIFT>(Hout + base + c, k[i], c, C);
             }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) h[i * VEC + e] = widen(k[i].v[e]);
         }
     }
     if (norm) {
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV * VEC; ++i) ss = fmaf(h[i], h[i], ss);
-        ss = row_reduce<false>(ss, tpr, red);
-        const float rs = rsqrtf(ss / float(C) + eps);
+        ss = row_reduce(ss, tpr, red, turn, [](float a, float b) { return a + b; });
+        const float rs = rsqrtf(fmaf(ss, invC, eps));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
+            const int c = col(i);
             float f[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) f[e] = 1.0f;
-            if (w && c < C) load_weight<VEC>(w + c, f);
+            if (w && has(c)) load_weight<VEC, SHIFT>(w, c, C, f);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) h[i * VEC + e] = h[i * VEC + e] * rs * f[e];
         }
@@ -172,141 +223,161 @@ __global__ void __launch_bounds__(kNormThreads)
     if constexpr (!I8) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
-            if (live && c < C) {
+            const int c = col(i);
+            if (has(c)) {
                 Pack<T, VEC> k;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) k.v[e] = narrow<T>(h[i * VEC + e]);
-                store_pack<T, VEC>(Y + base + c, k);
+                store_part<T, VEC, SHIFT>(Y + base + c, k, c, C);
             }
         }
     } else {
-        // a value that is not finite makes the maximum infinite: the row's scale becomes NaN and its values 0
-        float mx = 0.0f;
+        // absolute values as integers have the same order, with infinities and NaN above the finite ones: such a row has
+        // scale NaN and values 0
+        uint32_t mb = 0;
 #pragma unroll
         for (int i = 0; i < NV * VEC; ++i) {
-            const float a = fabsf(h[i]);
-            mx = fmaxf(mx, a <= FLT_MAX ? a : INFINITY);
+            const int c = col(i / VEC) + i % VEC;
+            const uint32_t a = __float_as_uint(h[i]) & 0x7FFFFFFFu;
+            mb = max(mb, !SHIFT || (c >= 0 && c < C) ? a : 0u);  // (0 * an infinite 1 / rms beside the row is NaN)
         }
-        mx = row_reduce<true>(mx, tpr, red);
-        const bool bad = mx > FLT_MAX;
-        const float s = bad ? nanf("") : mx / 127.0f;
+        mb = row_reduce(mb, tpr, redm, turn, [](uint32_t a, uint32_t b) { return max(a, b); });
+        const bool bad = mb >= 0x7F800000u;
+        const float s = bad ? nanf("") : __uint_as_float(mb) / 127.0f;
         if (live && t == 0) scale[row] = s;
-        const bool zero = bad || s == 0.0f;
+        // y / s correctly rounded, from the correctly rounded reciprocal and the exact remainders of the multiply-add
+        // (Markstein: from a quotient within one unit in the last place, one step gives the rounded one; the first step
+        // gets there).  Adding 1.5 * 2^23 then rounds to a whole number, whose low byte is the result.  Rows of extreme
+        // scale, of zeros or with values that are not finite are divided.
+        const bool quick = s >= 1e-25f && s <= 1e25f;
+        const float inv = 1.0f / s;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
-            if (live && c < C) {
+            const int c = col(i);
+            if (has(c)) {
                 Pack<int8_t, VEC> k;
+                if (quick) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float v = zero ? 0.0f : h[i * VEC + e] / s;
-                    k.v[e] = int8_t(max(-127, min(127, __float2int_rn(v))));
+                    for (int e = 0; e < VEC; ++e) {
+                        const float y = h[i * VEC + e];
+                        float q = y * inv;
+                        q = fmaf(fmaf(-q, s, y), inv, q);
+                        q = fmaf(fmaf(-q, s, y), inv, q);
+                        k.v[e] = int8_t(__float_as_int(q + 12582912.0f));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float v = bad || s == 0.0f ? 0.0f : h[i * VEC + e] / s;
+                        k.v[e] = int8_t(max(-127, min(127, __float2int_rn(v))));
+                    }
                 }
-                store_pack<int8_t, VEC>(Q + base + c, k);
+                store_part<int8_t, VEC, SHIFT>(Q + base + c, k, c, C);
             }
         }
     }
 }
 
-// Backward: every group of threads walks rows blockIdx.x * rpb + group, + gridDim.x * rpb, ...; a thread adds up
-// its columns' part of dw in registers, the block's groups add theirs in shared memory in the order of the groups,
-// and the block writes one row of `part` ([gridDim.x][C]).  k_norm_dw adds those rows in order, so that equal
-// calls give equal bits.
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(kNormThreads)
+constexpr int kBwdBlocks = 148 * 4;  // rows of partial sums of dw, at most
+
+// Backward: blocks of 256 threads on an SM; what their registers leave room for
+template <int VEC, int NV>
+constexpr int bwd_per_sm() { return NV * VEC <= 8 ? 3 : NV * VEC <= 16 ? 2 : 1; }
+
+// Backward: group G of tpr threads (of NG in the grid) walks rows G, G + NG, ...; NG is a multiple of VEC where there are
+// more rows than groups, so a group's rows have the same shift and a thread the same columns in all of them: it keeps its
+// part of the weight and of dw in registers.  The block's groups add theirs in shared memory in the order of the groups,
+// and the block writes one row of `part` ([gridDim.x][C]).  k_norm_dw adds those rows in order, so that equal calls give
+// equal bits.  PF: the next row is loaded before this one is reduced.
+template <typename T, int VEC, int NV, bool SHIFT>
+__global__ void __launch_bounds__(kNormThreads, bwd_per_sm<VEC, NV>())
     k_rms_norm_bwd(const T *dY, const T *dH, const T *H, const float *__restrict__ w, int64_t rows, int C,
-                               int tpr, float eps, T *dX, float *__restrict__ part)
+                   float invC, int tpr, float eps, T *dX, float *__restrict__ part)
 {
+    constexpr bool PF = NV == 1 && VEC > 1;
     extern __shared__ float acc_sm[];  // [groups][C] while the block's groups are joined
-    __shared__ float red[32];
+    __shared__ float2 red[16];
+    int turn = 0;
     const int rpb = int(blockDim.x) / tpr, t = int(threadIdx.x) % tpr, grp = int(threadIdx.x) / tpr;
-    float dw[NV * VEC];
+    const int64_t step = int64_t(gridDim.x) * rpb, G = int64_t(blockIdx.x) * rpb + grp;
+    const int sh = SHIFT ? int((size_t(G) * C) & (VEC - 1)) : 0;
+    auto col = [&](int i) { return (i * tpr + t) * VEC - sh; };
+    auto has = [&](int c) { return c < C && (!SHIFT || c + VEC > 0); };
+    float dw[NV * VEC], f[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV * VEC; ++i) dw[i] = 0.0f;
-    const int64_t step = int64_t(gridDim.x) * rpb;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = col(i);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[i][e] = 1.0f;
+        if (w && has(c)) load_weight<VEC, SHIFT>(w, c, C, f[i]);
+    }
+    struct Row {
+        Pack<T, VEC> h[NV], y[NV], u[NV];
+    };
+    auto fetch = [&](Row &k, int64_t row) {
+        const size_t base = size_t(row) * C;
+        load_row<SHIFT>(k.h, H + base, C, row < rows, row == rows - 1, col);
+        load_row<SHIFT>(k.y, dY + base, C, row < rows, row == rows - 1, col);
+        if (dH) load_row<SHIFT>(k.u, dH + base, C, row < rows, row == rows - 1, col);
+    };
+    Row k;
+    if (PF) fetch(k, G);
     // the block's groups take the same number of turns, so that the reductions find every thread
     for (int64_t r0 = int64_t(blockIdx.x) * rpb; r0 < rows; r0 += step) {
         const int64_t row = r0 + grp;
-        const bool live = row < rows;
-        const size_t base = live ? size_t(row) * C : 0;
-        Pack<T, VEC> hk[NV], yk[NV], uk[NV];
+        Row next;
+        if (PF) fetch(next, row + step);  // (dX may be dY or dH: another row's, written by nobody else)
+        else fetch(k, row);
+        float2 s = make_float2(0.0f, 0.0f);  // sums of h^2 and of g h
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
-            if (live && c < C) {
-                hk[i] = load_pack<T, VEC>(H + base + c);
-                yk[i] = load_pack<T, VEC>(dY + base + c);
-                if (dH) uk[i] = load_pack<T, VEC>(dH + base + c);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) hk[i].v[e] = yk[i].v[e] = narrow<T>(0.0f);
-            }
-        }
-        float ss = 0.0f, gh = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
-            float f[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) f[e] = 1.0f;
-            if (w && c < C) load_weight<VEC>(w + c, f);
+            mask_edge<SHIFT>(k.h[i], col(i), C);
+            mask_edge<SHIFT>(k.y[i], col(i), C);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float h = widen(hk[i].v[e]);
-                ss = fmaf(h, h, ss);
-                gh = fmaf(widen(yk[i].v[e]) * f[e], h, gh);
+                const float h = widen(k.h[i].v[e]);
+                s.x = fmaf(h, h, s.x);
+                s.y = fmaf(widen(k.y[i].v[e]) * f[i][e], h, s.y);
             }
         }
-        ss = row_reduce<false>(ss, tpr, red);
-        gh = row_reduce<false>(gh, tpr, red);
-        const float rs = rsqrtf(ss / float(C) + eps);
-        const float k2 = rs * rs * (gh / float(C));
+        s = row_reduce(s, tpr, red, turn, [](float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); });
+        const float rs = rsqrtf(fmaf(s.x, invC, eps));
+        const float k2 = rs * rs * (s.y * invC);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
-            if (live && c < C) {
-                float f[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) f[e] = 1.0f;
-                if (w) load_weight<VEC>(w + c, f);
-                Pack<T, VEC> k;
+            const int c = col(i);
+            if (row < rows && has(c)) {
+                Pack<T, VEC> o;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    const float h = widen(hk[i].v[e]), y = widen(yk[i].v[e]);
-                    float x = rs * (y * f[e] - h * k2);
-                    if (dH) x += widen(uk[i].v[e]);
-                    k.v[e] = narrow<T>(x);
+                    const float h = widen(k.h[i].v[e]), y = widen(k.y[i].v[e]);
+                    float x = rs * (y * f[i][e] - h * k2);
+                    if (dH) x += widen(k.u[i].v[e]);
+                    o.v[e] = narrow<T>(x);
                     dw[i * VEC + e] = fmaf(y, h * rs, dw[i * VEC + e]);
                 }
-                store_pack<T, VEC>(dX + base + c, k);
+                store_part<T, VEC, SHIFT>(dX + size_t(row) * C + c, o, c, C);
             }
         }
+        if (PF) k = next;
     }
     if (!part) return;
-    float *out = part + size_t(blockIdx.x) * C;
-    if (rpb == 1) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
-            if (c < C)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) out[c + e] = dw[i * VEC + e];
-        }
-        return;
-    }
+    float *out = rpb == 1 ? part + size_t(blockIdx.x) * C : acc_sm + grp * C;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + t) * VEC;
-        if (c < C)
+        const int c = col(i);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc_sm[grp * C + c + e] = dw[i * VEC + e];
+        for (int e = 0; e < VEC; ++e)
+            if (c + e >= 0 && c + e < C) out[c + e] = dw[i * VEC + e];
     }
+    if (rpb == 1) return;
     __syncthreads();
     for (int c = threadIdx.x; c < C; c += blockDim.x) {
         float a = 0.0f;
         for (int g = 0; g < rpb; ++g) a += acc_sm[g * C + c];
-        out[c] = a;
+        part[size_t(blockIdx.x) * C + c] = a;
     }
 }
 
@@ -318,7 +389,7 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float *__restrict__ part
     const int c = blockIdx.x * 32 + lane;
     float a = 0.0f;
     if (c < C)
-#pragma unroll 4
+#pragma unroll 8
         for (int r = wy; r < n; r += 32) a += part[size_t(r) * C + c];
     sm[wy][lane] = a;
     __syncthreads();
@@ -330,48 +401,58 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float *__restrict__ part
 
 struct NormShape {
     int vec, nv, tpr, threads;
+    bool shift;
 };
 
-// The widest vector that C and the addresses allow; then as few threads per row as hold it in NV <= 32 / VEC
-// vectors each when there are rows enough to fill the SMs, else as many as the row has vectors.
+// 16-byte vectors where the addresses are aligned (and the weight's, where the vectors follow its own), else single
+// elements.  Then the threads of a row:
+//   forward   as few as hold it in 32 / VEC vectors each, but four that share 64 bytes (a row per thread reads bytes far
+//             apart), when there are rows enough to fill the SMs; else as many as the row has vectors.  In 8 bits 16 / VEC
+//             where a warp is enough for that: there more of a row's time is arithmetic, and more threads hide it
+//             (1,048,576 x 128 bf16: 266 -> 205 us, but 170 -> 185 us with 16 bits out).
+//   backward  as many as the row has vectors, up to 256: a thread keeps its part of the weight and of dw, and one vector
+//             of each leaves room for the next row's.
 template <typename T>
-NormShape norm_shape(int64_t rows, int C, uintptr_t al, uintptr_t al_q, uintptr_t al_w)
+NormShape norm_shape(int64_t rows, int C, uintptr_t al, uintptr_t al_q, uintptr_t al_w, bool backward,
+                     bool i8 = false)
 {
-    const int es = int(sizeof(T));
+    constexpr int V = 16 / int(sizeof(T));
     NormShape s;
-    s.vec = 1;
-    for (int v = 16 / es; v > 1; v >>= 1) {
-        if (es == 2 && v == 4) continue;  // not instantiated
-        if (es == 4 && v == 2) continue;
-        if (C % v == 0 && al % uintptr_t(v * es) == 0 && al_q % uintptr_t(v) == 0 &&
-            al_w % uintptr_t(v >= 4 ? 16 : 4) == 0) {
-            s.vec = v;
-            break;
-        }
+    s.vec = V;
+    s.shift = C % V != 0;
+    auto vectors = [&] { return s.shift ? (C + 2 * (V - 1)) / V : C / s.vec; };  // of a row, at most
+    if (al % 16 != 0 || al_q % V != 0 || (!s.shift && al_w % 16 != 0) || vectors() > kMaxEpt / V * kNormThreads) {
+        s.vec = 1;
+        s.shift = false;
     }
-    const int cv = C / s.vec;                      // vectors per row
-    const int most = kMaxEpt / s.vec;              // vectors per thread
+    const int cv = vectors(), most = kMaxEpt / s.vec;  // vectors of a row, and of a thread at most
     int tpr = 1;
-    while (tpr * most < cv) tpr <<= 1;
-    // few rows: spread each over more threads, down to one vector each
-    while (tpr < cv && tpr < kNormThreads && rows * tpr < 148 * 512) tpr <<= 1;
+    if (backward) {
+        while (tpr < cv && tpr < kNormThreads) tpr <<= 1;
+    } else {
+        while ((i8 && tpr * most / 2 < cv && tpr < 32) || tpr * most < cv || (tpr < 4 && tpr < cv)) tpr <<= 1;
+        // few rows: spread each over more threads, down to one vector each
+        while (tpr < cv && tpr < kNormThreads && rows * tpr < 148 * 512) tpr <<= 1;
+    }
     s.tpr = tpr;
-    s.threads = tpr > 32 ? tpr : kNormThreads;  // a row of more than a warp has the block to itself
+    s.threads = kNormThreads;
+    if (!backward && tpr > 32) s.threads = tpr;  // a row of more than a warp has the block to itself
     const int need = (cv + tpr - 1) / tpr;
-    s.nv = need <= 1 ? 1 : need <= most / 4 ? most / 4 : most;
-    if (s.nv < 1) s.nv = 1;
+    s.nv = 1;
+    while (s.nv < need) s.nv <<= 1;
+    if (s.vec == 1 && s.nv > 1) s.nv = s.nv > 8 ? 32 : 8;
     return s;
 }
 
-template <typename T, int VEC, int NV, bool I8>
+template <typename T, int VEC, int NV, bool SHIFT, bool I8>
 bt_status run_norm(const NormShape &s, const void *X, const void *R, const float *w, int64_t rows, int C, float eps,
                    bool norm, void *Hout, void *Y, int8_t *Q, float *scale, cudaStream_t st)
 {
     const int rpb = s.threads / s.tpr;
     const int64_t grid = (rows + rpb - 1) / rpb;
     if (grid > 0x7FFFFFFF) return BT_ERR_UNSUPPORTED;
-    k_rms_norm<T, VEC, NV, I8><<<unsigned(grid), s.threads, 0, st>>>(
-        static_cast<const T *>(X), static_cast<const T *>(R), w, rows, C, s.tpr, eps, norm, static_cast<T *>(Hout),
+    k_rms_norm<T, VEC, NV, SHIFT, I8><<<unsigned(grid), s.threads, 0, st>>>(
+        static_cast<const T *>(X), static_cast<const T *>(R), w, rows, C, 1.0f / float(C), s.tpr, eps, norm, static_cast<T *>(Hout),
         static_cast<T *>(Y), Q, scale);
     return cudaPeekAtLastError() == cudaSuccess ? BT_OK : BT_ERR_CUDA;
 }
@@ -382,31 +463,41 @@ bt_status launch_norm(const void *X, const void *R, const float *w, int64_t rows
 {
     const uintptr_t al = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(R) |
                          reinterpret_cast<uintptr_t>(Hout) | reinterpret_cast<uintptr_t>(Y);
-    const NormShape s = norm_shape<T>(rows, C, al, reinterpret_cast<uintptr_t>(Q), reinterpret_cast<uintptr_t>(w));
-#define BTS_NORM(V, N)                                                                                     \
-    if (s.vec == V && s.nv == N)                                                                           \
-        return run_norm<T, V, N, I8>(s, X, R, w, rows, C, eps, norm, Hout, Y, Q, scale, st);
+    const NormShape s =
+        norm_shape<T>(rows, C, al, reinterpret_cast<uintptr_t>(Q), reinterpret_cast<uintptr_t>(w), false, I8);
+#define BTS_NORM(V, N, S)                                                                                  \
+    if (s.vec == V && s.nv == N && s.shift == S)                                                           \
+        return run_norm<T, V, N, S, I8>(s, X, R, w, rows, C, eps, norm, Hout, Y, Q, scale, st);
     if constexpr (sizeof(T) == 2) {
-        BTS_NORM(8, 1) BTS_NORM(8, 4) BTS_NORM(2, 1) BTS_NORM(2, 4) BTS_NORM(2, 16)
+        BTS_NORM(8, 1, false) BTS_NORM(8, 2, false) BTS_NORM(8, 4, false)
+        BTS_NORM(8, 1, true) BTS_NORM(8, 2, true) BTS_NORM(8, 4, true)
     } else {
-        BTS_NORM(4, 1) BTS_NORM(4, 2) BTS_NORM(4, 8)
+        BTS_NORM(4, 1, false) BTS_NORM(4, 2, false) BTS_NORM(4, 4, false) BTS_NORM(4, 8, false)
+        BTS_NORM(4, 1, true) BTS_NORM(4, 2, true) BTS_NORM(4, 4, true) BTS_NORM(4, 8, true)
     }
-    BTS_NORM(1, 1) BTS_NORM(1, 8) BTS_NORM(1, 32)
+    BTS_NORM(1, 1, false) BTS_NORM(1, 8, false) BTS_NORM(1, 32, false)
 #undef BTS_NORM
     return BT_ERR_INTERNAL;
 }
 
-constexpr int kBwdBlocks = 148 * 4;  // rows of partial sums of dw
 
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, int NV, bool SHIFT>
 bt_status run_bwd(const NormShape &s, const void *dY, const void *dH, const void *H, const float *w, int64_t rows,
-                  int C, float eps, void *dX, float *part, int64_t blocks, cudaStream_t st)
+                  int C, float eps, void *dX, float *part, int64_t &blocks, cudaStream_t st)
 {
+    int dev = 0;
+    const int sms = device_sms(&dev);
+    if (sms == 0) return BT_ERR_CUDA;
     const int rpb = s.threads / s.tpr;
+    // one wave; a multiple of 8 blocks, and so of 8 groups, where a group has several rows
+    int64_t most = int64_t(sms) * bwd_per_sm<VEC, NV>() / 8 * 8;
+    most = most < 8 ? 8 : most > kBwdBlocks ? kBwdBlocks : most;
+    blocks = (rows + rpb - 1) / rpb;
+    if (blocks > most) blocks = most;
     const size_t smem = part && rpb > 1 ? size_t(rpb) * C * 4 : 0;
     // rpb * C <= threads / tpr * tpr * 32 values: at most 32 KB
-    k_rms_norm_bwd<T, VEC, NV><<<unsigned(blocks), s.threads, smem, st>>>(
-        static_cast<const T *>(dY), static_cast<const T *>(dH), static_cast<const T *>(H), w, rows, C, s.tpr, eps,
+    k_rms_norm_bwd<T, VEC, NV, SHIFT><<<unsigned(blocks), s.threads, smem, st>>>(
+        static_cast<const T *>(dY), static_cast<const T *>(dH), static_cast<const T *>(H), w, rows, C, 1.0f / float(C), s.tpr, eps,
         static_cast<T *>(dX), part);
     return cudaPeekAtLastError() == cudaSuccess ? BT_OK : BT_ERR_CUDA;
 }
@@ -419,19 +510,19 @@ bt_status launch_bwd(const void *dY, const void *dH, const void *H, const float 
                          reinterpret_cast<uintptr_t>(H) | reinterpret_cast<uintptr_t>(dX);
     int64_t blocks = 0;
     if (rows > 0) {
-        const NormShape s = norm_shape<T>(rows, C, al, 0, reinterpret_cast<uintptr_t>(w));
-        const int rpb = s.threads / s.tpr;
-        blocks = (rows + rpb - 1) / rpb;
-        if (blocks > kBwdBlocks) blocks = kBwdBlocks;
+        const NormShape s = norm_shape<T>(rows, C, al, 0, reinterpret_cast<uintptr_t>(w), true);
         bt_status r = BT_ERR_INTERNAL;
-#define BTS_BWD(V, N) \
-    if (s.vec == V && s.nv == N) r = run_bwd<T, V, N>(s, dY, dH, H, w, rows, C, eps, dX, dw ? part : nullptr, blocks, st);
+#define BTS_BWD(V, N, S)                         \
+    if (s.vec == V && s.nv == N && s.shift == S) \
+        r = run_bwd<T, V, N, S>(s, dY, dH, H, w, rows, C, eps, dX, dw ? part : nullptr, blocks, st);
         if constexpr (sizeof(T) == 2) {
-            BTS_BWD(8, 1) BTS_BWD(8, 4) BTS_BWD(2, 1) BTS_BWD(2, 4) BTS_BWD(2, 16)
+            BTS_BWD(8, 1, false) BTS_BWD(8, 2, false) BTS_BWD(8, 4, false)
+            BTS_BWD(8, 1, true) BTS_BWD(8, 2, true) BTS_BWD(8, 4, true)
         } else {
-            BTS_BWD(4, 1) BTS_BWD(4, 2) BTS_BWD(4, 8)
+            BTS_BWD(4, 1, false) BTS_BWD(4, 2, false) BTS_BWD(4, 4, false) BTS_BWD(4, 8, false)
+            BTS_BWD(4, 1, true) BTS_BWD(4, 2, true) BTS_BWD(4, 4, true) BTS_BWD(4, 8, true)
         }
-        BTS_BWD(1, 1) BTS_BWD(1, 8) BTS_BWD(1, 32)
+        BTS_BWD(1, 1, false) BTS_BWD(1, 8, false) BTS_BWD(1, 32, false)
 #undef BTS_BWD
         if (r != BT_OK) return r;
     }
