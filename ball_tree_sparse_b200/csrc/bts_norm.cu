@@ -280,21 +280,27 @@ __global__ void __launch_bounds__(kNormThreads)
 
 constexpr int kBwdBlocks = 148 * 4;  // rows of partial sums of dw, at most
 
-// Backward: blocks of 256 threads on an SM; what their registers leave room for
-template <int VEC, int NV>
-constexpr int bwd_per_sm() { return NV * VEC <= 8 ? 3 : NV * VEC <= 16 ? 2 : 1; }
+// Backward: whether the next row is loaded before a row is reduced, and blocks of 256 threads on an SM (what their registers
+// leave room for).  Floats: two vectors a thread, two blocks, the next row ahead (65,536 x 512: 94 us; one vector, no row
+// ahead, four blocks: 107).  16 bits have twice the arithmetic to a byte, and more threads do better than rows ahead
+// (65,536 x 1024: 123 us with one vector and four blocks; 143 with three and a row ahead).
+template <typename T, int VEC, int NV>
+struct BwdShape {
+    static constexpr bool AHEAD = sizeof(T) == 4 && NV <= 2 && VEC > 1;
+    static constexpr int PER_SM = NV * VEC <= 8 ? (AHEAD ? 2 : 4) : NV * VEC <= 16 ? 2 : 1;
+};
 
 // Backward: group G of tpr threads (of NG in the grid) walks rows G, G + NG, ...; NG is a multiple of VEC where there are
 // more rows than groups, so a group's rows have the same shift and a thread the same columns in all of them: it keeps its
 // part of the weight and of dw in registers.  The block's groups add theirs in shared memory in the order of the groups,
 // and the block writes one row of `part` ([gridDim.x][C]).  k_norm_dw adds those rows in order, so that equal calls give
-// equal bits.  PF: the next row is loaded before this one is reduced.
+// equal bits.
 template <typename T, int VEC, int NV, bool SHIFT>
-__global__ void __launch_bounds__(kNormThreads, bwd_per_sm<VEC, NV>())
+__global__ void __launch_bounds__(kNormThreads, (BwdShape<T, VEC, NV>::PER_SM))
     k_rms_norm_bwd(const T *dY, const T *dH, const T *H, const float *__restrict__ w, int64_t rows, int C,
                    float invC, int tpr, float eps, T *dX, float *__restrict__ part)
 {
-    constexpr bool PF = NV == 1 && VEC > 1;
+    constexpr bool PF = BwdShape<T, VEC, NV>::AHEAD;
     extern __shared__ float acc_sm[];  // [groups][C] while the block's groups are joined
     __shared__ float2 red[16];
     int turn = 0;
@@ -410,8 +416,7 @@ struct NormShape {
 //             apart), when there are rows enough to fill the SMs; else as many as the row has vectors.  In 8 bits 16 / VEC
 //             where a warp is enough for that: there more of a row's time is arithmetic, and more threads hide it
 //             (1,048,576 x 128 bf16: 266 -> 205 us, but 170 -> 185 us with 16 bits out).
-//   backward  as many as the row has vectors, up to 256: a thread keeps its part of the weight and of dw, and one vector
-//             of each leaves room for the next row's.
+//   backward  a vector each, or two of floats, up to 256 threads: a thread keeps its part of the weight and of dw.
 template <typename T>
 NormShape norm_shape(int64_t rows, int C, uintptr_t al, uintptr_t al_q, uintptr_t al_w, bool backward,
                      bool i8 = false)
@@ -428,7 +433,7 @@ NormShape norm_shape(int64_t rows, int C, uintptr_t al, uintptr_t al_q, uintptr_
     const int cv = vectors(), most = kMaxEpt / s.vec;  // vectors of a row, and of a thread at most
     int tpr = 1;
     if (backward) {
-        while (tpr < cv && tpr < kNormThreads) tpr <<= 1;
+        while (tpr * (sizeof(T) == 4 ? 2 : 1) < cv && tpr < kNormThreads) tpr <<= 1;
     } else {
         while ((i8 && tpr * most / 2 < cv && tpr < 32) || tpr * most < cv || (tpr < 4 && tpr < cv)) tpr <<= 1;
         // few rows: spread each over more threads, down to one vector each
@@ -490,7 +495,7 @@ bt_status run_bwd(const NormShape &s, const void *dY, const void *dH, const void
     if (sms == 0) return BT_ERR_CUDA;
     const int rpb = s.threads / s.tpr;
     // one wave; a multiple of 8 blocks, and so of 8 groups, where a group has several rows
-    int64_t most = int64_t(sms) * bwd_per_sm<VEC, NV>() / 8 * 8;
+    int64_t most = int64_t(sms) * (BwdShape<T, VEC, NV>::PER_SM) / 8 * 8;
     most = most < 8 ? 8 : most > kBwdBlocks ? kBwdBlocks : most;
     blocks = (rows + rpb - 1) / rpb;
     if (blocks > most) blocks = most;

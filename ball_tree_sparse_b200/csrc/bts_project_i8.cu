@@ -213,21 +213,22 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------------------
 // Tensor cores (tcgen05.mma kind::i8, 32-bit integer sums in TMEM).  A CTA keeps to one chunk of BN output channels and
 // walks the 128-row tiles of X:
-//   warps 9-12  loaders.  TMA: one thread fetches 128 x 128-byte boxes (128-byte swizzle; rows and columns outside read
+//   warps 17-20  loaders.  TMA: one thread fetches 128 x 128-byte boxes (128-byte swizzle; rows and columns outside read
 //               zeros).  Otherwise (row lengths or addresses that no tensor map takes) the four warps copy 16 bytes a
 //               thread, put together from aligned words.
-//   warp 8      issues the products, two accumulators of BN columns;
-//   warps 0-7   two warps per 32 rows, each half of the columns: scale, round, pass through 4 KB of shared memory of
-//               the warp's own, and store 128-byte pieces of rows to the row's slot of Q, K or V.
+//   warp 16      issues the products, two accumulators of BN columns;
+//   warps 0-15   four warps per 32 rows, a quarter of the columns (but at least 32) each: scale, round, pass through
+//                4 KB of shared memory of the warp's own, and store 128-byte pieces of rows to the row's slot of Q, K
+//                or V.
 // W stays in shared memory where the chunk's rows fit (`keep`), else it is fetched with each block of X.
 // Bound by the stores: 65,536 x 256 -> 768 bf16 in tree order is 118 MB, 18 us.
 // ---------------------------------------------------------------------------
 struct I8Tile {
-    static constexpr int BM = 128, BK = 128, THREADS = 13 * 32;
+    static constexpr int BM = 128, BK = 128, EPI = 16, THREADS = (EPI + 5) * 32;
     static constexpr uint32_t XBLK = BM * BK;
-    static constexpr uint32_t OUT = 8 * 4096;                       // the epilogue's pieces
-    static constexpr uint32_t ROOM = 220 * 1024 - OUT - 1024;       // for W and the ring
-    static constexpr int RING = 6;                                  // stages, at most
+    static constexpr uint32_t OUT = EPI * 4096;      // the epilogue's pieces
+    static constexpr uint32_t ROOM = 160 * 1024;     // for W and the ring
+    static constexpr int RING = 6;                   // stages, at most
 };
 
 __device__ __forceinline__ void mma_i8(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             init(&sAccFull[i], 1);
-            init(&sAccEmpty[i], 8);
+            init(&sAccEmpty[i], L::EPI);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -331,9 +332,9 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = sTmem;
 
-    if (warp >= 9) {
+    if (warp > L::EPI) {
         if (TMA) {
-            if (warp == 9 && lane == 0) {
+            if (warp == L::EPI + 1 && lane == 0) {
                 bool ok = true;
                 if (keep) {
                     mbar_expect_tx(smem_u32(&sWFull), uint32_t(KB) * WBLK);
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
                     mbar_wait(smem_u32(&sFull[k % stages]), (k / stages) & 1, status);
             }
         } else {
-            const int lt = tid - 9 * 32;  // 0 .. 127
+            const int lt = tid - (L::EPI + 1) * 32;  // 0 .. 127
             auto block = [&](const int8_t *M, int64_t n, int64_t r0, int nr, int k, uint32_t off) {
 #pragma unroll 4
                 for (int u = lt; u < nr * 8; u += 128) {
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
                 }
         }
         __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == L::EPI) {
         // ---------------- products (one thread) ----------------
         if (lane == 0) {
             bool ok = !keep || mbar_wait(smem_u32(&sWFull), 0, status);
@@ -423,7 +424,8 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
         // ---------------- epilogue ----------------
         constexpr int PC = 128 / int(sizeof(T));      // columns of a piece (128 bytes)
         constexpr int CE = 16 / int(sizeof(T));       // columns of a chunk (16 bytes)
-        const int half = warp >> 2;
+        constexpr int CW = BN >= 128 ? BN / 4 : 32;   // columns of a warp
+        const int quarter = warp >> 2;
         const uint32_t lb = uint32_t((warp & 3) * 32) << 16;
         uint8_t *piece = gbase + warp * 4096;
         bool ok = true;
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
                 xr = __ldg(xs + row);
                 orow = inv ? __ldg(inv + row) : int32_t(row);
                 if (inv && (orow < 0 || orow >= npad)) {  // not a slot: never write it
-                    if (half == 0 && chunk == 0) record_error(status, BT_ERR_INTERNAL);
+                    if (quarter == 0 && chunk == 0) record_error(status, BT_ERR_INTERNAL);
                     orow = -1;
                 }
             }
@@ -444,14 +446,14 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
             ok = mbar_wait(smem_u32(&sAccFull[ab]), (ai >> 1) & 1, status);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
-            const uint32_t acc = tmem + uint32_t(ab) * BN + uint32_t(half * (BN / 2)) + lb;
+            const uint32_t acc = tmem + uint32_t(ab) * BN + uint32_t(quarter * CW) + lb;
 #pragma unroll 1
-            for (int c0 = 0; c0 < BN / 2; c0 += PC) {
-                const int jl = half * (BN / 2) + c0, j0 = chunk * BN + jl;
-                if (j0 >= nout || !ok) break;  // the same for every thread of the warp
+            for (int c0 = 0; c0 < CW; c0 += PC) {
+                const int jl = quarter * CW + c0, j0 = chunk * BN + jl;
+                if (jl >= BN || j0 >= nout || !ok) break;  // the same for every thread of the warp
 #pragma unroll
                 for (int q = 0; q < PC; q += 32) {
-                    if (c0 + q >= BN / 2) break;
+                    if (c0 + q >= CW) break;
                     uint32_t v[32];
                     tmem_ld32_nowait(acc + c0 + q, v);
                     tmem_wait_ld();
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
                 __syncwarp();
                 // 4 rows of 128 bytes at a time
                 const int c = lane & 7, j = j0 + c * CE;
-                const bool in = c * CE < BN / 2 - c0 && j < nout;  // 3 H d is a multiple of a chunk
+                const bool in = c * CE < CW - c0 && j < nout;  // 3 H d is a multiple of a chunk
                 const int t = j / out.hd;
                 T *dst = (t == 0 ? out.q : t == 1 ? out.k : out.v) + (j - t * out.hd);
 #pragma unroll
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
             __syncwarp();
             if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sAccEmpty[ab])) : "memory");
         }
-        if (perm) zero_dummies(perm, npad, out, int64_t(blockIdx.x) * 8 + warp, int64_t(gridDim.x) * 8);
+        if (perm) zero_dummies(perm, npad, out, int64_t(blockIdx.x) * L::EPI + warp, int64_t(gridDim.x) * L::EPI);
     }
     tc_fence_before();
     __syncthreads();
@@ -552,7 +554,7 @@ bt_status run_project_tc(const I8Args<T> &a)
         return BT_ERR_CUDA;
     const int KB = (a.C + L::BK - 1) / L::BK;
     const int64_t wbytes = int64_t(KB) * BN * L::BK;
-    const bool keep = wbytes + 3 * int64_t(L::XBLK) <= int64_t(L::ROOM);  // and three stages beside it
+    const bool keep = wbytes + 2 * int64_t(L::XBLK) <= int64_t(L::ROOM);  // and two stages beside it
     const uint32_t stage = L::XBLK + (keep ? 0 : BN * L::BK);
     int stages = int((L::ROOM - (keep ? uint32_t(wbytes) : 0)) / stage);
     if (stages > L::RING) stages = L::RING;
