@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(256)
 //                4 KB of shared memory of the warp's own, and store 128-byte pieces of rows to the row's slot of Q, K
 //                or V.
 // W stays in shared memory where the chunk's rows fit (`keep`), else it is fetched with each block of X.
-// Bound by the stores: 65,536 x 256 -> 768 bf16 in tree order is 118 MB, 18 us.
+// Bound by the integer products: 65,536 x 256 -> 768 keeps the tensor pipe active for 23 us (4,096 operations a cycle and
+// SM, half of what bf16 has); its 118 MB take 18 us.
 // ---------------------------------------------------------------------------
 struct I8Tile {
     static constexpr int BM = 128, BK = 128, EPI = 16, THREADS = (EPI + 5) * 32;
@@ -334,6 +335,8 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
 
     if (warp > L::EPI) {
         if (TMA) {
+            if (perm && warp > L::EPI + 1)  // these three have nothing to load
+                zero_dummies(perm, npad, out, int64_t(blockIdx.x) * 3 + warp - L::EPI - 2, int64_t(gridDim.x) * 3);
             if (warp == L::EPI + 1 && lane == 0) {
                 bool ok = true;
                 if (keep) {
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
             __syncwarp();
             if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sAccEmpty[ab])) : "memory");
         }
-        if (perm) zero_dummies(perm, npad, out, int64_t(blockIdx.x) * L::EPI + warp, int64_t(gridDim.x) * L::EPI);
+        if (!TMA && perm) zero_dummies(perm, npad, out, int64_t(blockIdx.x) * L::EPI + warp, int64_t(gridDim.x) * L::EPI);
     }
     tc_fence_before();
     __syncthreads();
