@@ -337,6 +337,13 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[1
                  : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_ld_nowait(uint32_t taddr, uint32_t (&r)[N])
 {
@@ -464,7 +471,7 @@ __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
 }
 
-template <int D>
+template <int D, bool MULTI>
 __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
     k_ball_bwd_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
@@ -489,6 +496,7 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
     __shared__ int32_t sRows[2][128];
     __shared__ uint32_t sMask[2][4];  // real slots of the tile
     __shared__ int32_t sItem[2];      // -1: no more work
+    __shared__ int32_t sWhole[2];     // no dummies among the tile's 128 slots
     __shared__ float sX[2][2][3][128];  // per group and half: a row's max, sum and sum of e dP
     __shared__ int32_t sOut[2][128];  // d = 32: rows of the results in the buffer
     __shared__ uint32_t sTmem;
@@ -609,7 +617,7 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
                             mma_ss(tS + L::T_V, p0 + 128 * kk, DESC_P, s0 + (3 * L::TENSOR + 2048 * kk) / 16, DESC,
                                    IDESC_T, kk > 0);
                         mma_commit(barV);
-                        if (OWN && spt <= m) mma_commit(smem_u32(&sEmpty[st][1]));
+                        if (OWN && !MULTI) mma_commit(smem_u32(&sEmpty[st][1]));
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             mma_ts(tS + L::T_Q, tS + L::T_G + 64 * (kk >> 2) + 8 * (kk & 3), s0 + (L::TENSOR + 2048 * kk) / 16, DESC, IDESC_Q, kk > 0);
@@ -631,7 +639,7 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
                         for (int kk = 0; kk < 8; ++kk)
                             mma_ss(tS + L::T_K, p0 + 128 * kk, DESC_P, s0 + 128 * kk, DESC, IDESC_T, kk > 0);
                         mma_commit(barO);
-                        if (spt <= m) {  // the stage is free once these products are done
+                        if (!MULTI) {  // the stage is free once these products are done
                             mma_commit(smem_u32(&sEmpty[st][0]));
                             if (!OWN) mma_commit(smem_u32(&sEmpty[st][1]));
                         }
@@ -707,10 +715,14 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
                             sRows[st][4 * lane + i] = cur[i];
                             nib |= uint32_t(cur[i] >= 0) << i;
                         }
+                        const bool whole = __all_sync(0xffffffffu, nib == 15u);
                         nib <<= 4 * (lane & 7);
                         for (int o = 1; o < 8; o <<= 1) nib |= __shfl_xor_sync(0xffffffffu, nib, o);
                         if ((lane & 7) == 0) sMask[st][lane >> 3] = nib;
-                        if (lane == 0) sItem[st] = item;
+                        if (lane == 0) {
+                            sItem[st] = item;
+                            sWhole[st] = whole;
+                        }
                         __syncwarp();
                         // arrive (release): the rows, the mask and the item are there; then the bytes of the gathers
                         if (lane == 0) mbar_expect_tx(full, 2 * L::TENSOR);
@@ -748,7 +760,6 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
     } else {
         // ---------------- one head: query row (and key row) r, keys and columns of half `half` ----------------
         const int g = warp >> 3, half = (warp >> 2) & 1, r = tid & 127;
-        const bool multi = spt > m;  // several balls in a tile
         const uint32_t tS = tmem + L::TMEM * g + (uint32_t((warp & 3) * 32) << 16), tG = tS + L::T_G;
         const uint32_t tV = tS + L::T_V, tQ = tS + L::T_Q, tK = tS + L::T_K;
         const uint32_t barS = smem_u32(&sBarS[g]), barG = smem_u32(&sBarG[g]), barV = smem_u32(&sBarV[g]),
@@ -821,122 +832,122 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
             const int item = sItem[st];
             if (sAbort[g] || item < 0) break;
             const int32_t row = sRows[st][r];
-            // the keys of this thread's two groups of 32 that count, and for the warp: bit c, some count in group c;
-            // bit 2 + c, all
-            uint32_t cm[2];
-            int some = 0, all = 0;
+            // the keys of this thread's two groups of 32 that count; several balls: and for the warp, bit c, some count in
+            // group c, bit c of all: all
+            uint32_t cm[2] = {0xffffffffu, 0xffffffffu};
+            [[maybe_unused]] int some = 3, all = 3;
+            const bool whole = !MULTI && sWhole[st];
+            if (!whole) {
+                some = all = 0;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int k0 = half * 64 + c * 32;
-                const int lo = max(b0 - k0, 0), hi = min(b1 - k0, 32);
-                const uint32_t in = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
-                cm[c] = row >= 0 ? in & sMask[st][half * 2 + c] : 0u;
-                some |= int(__any_sync(0xffffffffu, cm[c] != 0u)) << c;
-                all |= int(__all_sync(0xffffffffu, cm[c] == 0xffffffffu)) << c;
+                for (int c = 0; c < 2; ++c) {
+                    const int k0 = half * 64 + c * 32;
+                    const int lo = max(b0 - k0, 0), hi = min(b1 - k0, 32);
+                    const uint32_t in = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
+                    cm[c] = row >= 0 ? in & sMask[st][half * 2 + c] : 0u;
+                    if (MULTI) {
+                        some |= int(__any_sync(0xffffffffu, cm[c] != 0u)) << c;
+                        all |= int(__all_sync(0xffffffffu, cm[c] == 0xffffffffu)) << c;
+                    }
+                }
             }
-            // e = exp2(s - max) over S, the maximum and the sums of e and e dP by groups of 32 keys
-            float mc[2], sc[2], lc[2];
+            // e = exp2(s - max) over S, the maximum and the sums of e and e dP by groups of 32 keys.  The loops are not
+            // unrolled: the instruction cache and the registers of 640 threads are short.
+            float m0 = -INFINITY, m1 = -INFINITY, s0 = 0.0f, s1 = 0.0f, l0 = 0.0f, l1 = 0.0f;
             if (ok) ok = mbar_wait(barS, par, status);
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 2; ++c) {
-                mc[c] = -INFINITY;
-                sc[c] = lc[c] = 0.0f;
-                if (!((some >> c) & 1)) continue;
+                if (MULTI && !((some >> c) & 1)) continue;
+                const uint32_t on = c ? cm[1] : cm[0];
                 uint32_t e[32], v[32];
                 tmem_ld32_nowait(tS + half * 64 + c * 32, e);
                 tmem_wait_ld();
-                float s1 = 0.0f, l1 = 0.0f;
-                if ((all >> c) & 1) {
-                    float m1 = -INFINITY;
+                float mx = -INFINITY, sa = 0.0f, sb = 0.0f, la = 0.0f, lb = 0.0f;
+                const bool full = MULTI ? (all >> c) & 1 : whole;
+                // one ball: what is no key is a dummy, whose rows are zeros, so that only S needs the mask
+                if (!full) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (!((on >> j) & 1u)) e[j] = __float_as_uint(-INFINITY);
+                }
+                {
+                    float my = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        mc[c] = fmax3(mc[c], __uint_as_float(e[j]), __uint_as_float(e[j + 1]));
-                        m1 = fmax3(m1, __uint_as_float(e[j + 2]), __uint_as_float(e[j + 3]));
+                        mx = fmax3(mx, __uint_as_float(e[j]), __uint_as_float(e[j + 1]));
+                        my = fmax3(my, __uint_as_float(e[j + 2]), __uint_as_float(e[j + 3]));
                     }
-                    mc[c] = fmaxf(mc[c], m1);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if ((cm[c] >> j) & 1u) mc[c] = fmaxf(mc[c], __uint_as_float(e[j]));
+                    mx = fmaxf(mx, my);
                 }
-                const float mxs = mc[c] == -INFINITY ? 0.0f : mc[c] * sl2;
-                if (c == 0 || !(some & 1)) {
-                    if (ok) ok = mbar_wait(barG, par, status);
-                    tc_fence_after();
-                }
+                const float mxs = mx == -INFINITY ? 0.0f : mx * sl2;
+                if (ok) ok = mbar_wait(barG, par, status);
+                tc_fence_after();
                 tmem_ld32_nowait(tG + half * 64 + c * 32, v);
-                if ((all >> c) & 1) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float p0, p1;
-                        ffma2_bcast(__uint_as_float(e[j]), __uint_as_float(e[j + 1]), sl2, -mxs, p0, p1);
-                        e[j] = __float_as_uint(ex2(p0));
-                        e[j + 1] = __float_as_uint(ex2(p1));
-                        fadd2_acc(sc[c], s1, __uint_as_float(e[j]), __uint_as_float(e[j + 1]));
+                for (int j = 0; j < 32; j += 2) {
+                    float p0, p1;
+                    ffma2_bcast(__uint_as_float(e[j]), __uint_as_float(e[j + 1]), sl2, -mxs, p0, p1);
+                    e[j] = __float_as_uint(ex2(p0));
+                    e[j + 1] = __float_as_uint(ex2(p1));
+                    if (MULTI && !full) {  // (a row whose maximum is infinite has NaN beside it too)
+                        e[j] = (on >> j) & 1u ? e[j] : 0u;
+                        e[j + 1] = (on >> (j + 1)) & 1u ? e[j + 1] : 0u;
                     }
-                    tmem_st<32>(tS + half * 64 + c * 32, e);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        ffma2_acc(lc[c], l1, __uint_as_float(e[j]), __uint_as_float(e[j + 1]), __uint_as_float(v[j]),
-                                  __uint_as_float(v[j + 1]));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float p = ex2(fmaf(__uint_as_float(e[j]), sl2, -mxs));
-                        e[j] = (cm[c] >> j) & 1u ? __float_as_uint(p) : 0u;
-                        sc[c] += __uint_as_float(e[j]);
-                    }
-                    tmem_st<32>(tS + half * 64 + c * 32, e);
-                    tmem_wait_ld();
+                    fadd2_acc(sa, sb, __uint_as_float(e[j]), __uint_as_float(e[j + 1]));
+                }
+                tmem_st<32>(tS + half * 64 + c * 32, e);
+                tmem_wait_ld();
+                if (MULTI && !full) {  // another ball's dP may be anything
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if ((cm[c] >> j) & 1u) lc[c] = fmaf(__uint_as_float(e[j]), __uint_as_float(v[j]), lc[c]);
+                        if (!((on >> j) & 1u)) v[j] = 0u;
                 }
-                sc[c] += s1;
-                lc[c] += l1;
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+                    ffma2_acc(la, lb, __uint_as_float(e[j]), __uint_as_float(e[j + 1]), __uint_as_float(v[j]),
+                              __uint_as_float(v[j + 1]));
+                if (c) { m1 = mx; s1 = sa + sb; l1 = la + lb; }
+                else { m0 = mx; s0 = sa + sb; l0 = la + lb; }
             }
-            if (ok) ok = mbar_wait(barG, par, status);  // a warp without keys: dS comes over dP
-            float fs[2], delta;  // P = e fs
+            if (MULTI && ok) ok = mbar_wait(barG, par, status);  // a warp without keys: dS comes over dP
+            float f0, f1, delta;  // P = e f0 in the first group, e f1 in the second
             {
                 // sums over a part without keys count for nothing, whatever they hold
-                const float mx = fmaxf(mc[0], mc[1]);
-                float f[2], den = 0.0f, dl = 0.0f;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    f[c] = mc[c] == -INFINITY ? 0.0f : ex2((mc[c] - mx) * sl2);
-                    if (cm[c]) { den = fmaf(sc[c], f[c], den); dl = fmaf(lc[c], f[c], dl); }
-                }
+                const float mx = fmaxf(m0, m1);
+                f0 = m0 == -INFINITY ? 0.0f : ex2((m0 - mx) * sl2);
+                f1 = m1 == -INFINITY ? 0.0f : ex2((m1 - mx) * sl2);
+                float den = 0.0f, dl = 0.0f;
+                if (cm[0]) { den = s0 * f0; dl = l0 * f0; }
+                if (cm[1]) { den = fmaf(s1, f1, den); dl = fmaf(l1, f1, dl); }
                 sX[g][half][0][r] = mx;
                 sX[g][half][1][r] = den;
                 sX[g][half][2][r] = dl;
                 named_sync<64>(pair);
                 const float mo = sX[g][half ^ 1][0][r], so = sX[g][half ^ 1][1][r], lo = sX[g][half ^ 1][2][r];
                 const float M = fmaxf(mx, mo);
-                const float f0 = mx == -INFINITY ? 0.0f : ex2((mx - M) * sl2);
-                const float f1 = mo == -INFINITY ? 0.0f : ex2((mo - M) * sl2);
-                den *= f0;
-                dl *= f0;
-                if (so != 0.0f) { den = fmaf(so, f1, den); dl = fmaf(lo, f1, dl); }
+                const float g0 = mx == -INFINITY ? 0.0f : ex2((mx - M) * sl2);
+                const float g1 = mo == -INFINITY ? 0.0f : ex2((mo - M) * sl2);
+                den *= g0;
+                dl *= g0;
+                if (so != 0.0f) { den = fmaf(so, g1, den); dl = fmaf(lo, g1, dl); }
                 const float inv = row >= 0 ? 1.0f / den : 0.0f;
-                fs[0] = f[0] * f0 * inv;
-                fs[1] = f[1] * f0 * inv;
+                f0 *= g0 * inv;
+                f1 *= g0 * inv;
                 delta = dl * inv;
             }
             if (!OWN && it > 0 && ok) ok = mbar_wait(smem_u32(&sBarF[g]), (it - 1) & 1, status);  // results are stored
             tmem_wait_st();
-            uint32_t ds[32];
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-                uint32_t w[8];
-                if ((some >> (c >> 1)) & 1) {
+                uint32_t w[8], ds[8];
+                if (!MULTI || ((some >> (c >> 1)) & 1)) {
                     uint32_t e[16], v[16];
-                    const float f = fs[c >> 1];
+                    const float f = c < 2 ? f0 : f1;
                     tmem_ld16_nowait(tS + half * 64 + c * 16, e);
                     tmem_ld16_nowait(tG + half * 64 + c * 16, v);
                     tmem_wait_ld();
-                    if ((all >> (c >> 1)) & 1) {
+                    if (!MULTI || ((all >> (c >> 1)) & 1)) {
 #pragma unroll
                         for (int k = 0; k < 16; k += 2) {
                             float p0, p1, d0, d1;
@@ -944,35 +955,35 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
                             fadd2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]), -delta, -delta, d0, d1);
                             fmul2(p0, p1, d0, d1, d0, d1);
                             w[k >> 1] = pack_bf16(p0, p1);
-                            ds[c * 8 + (k >> 1)] = pack_bf16(d0, d1);
+                            ds[k >> 1] = pack_bf16(d0, d1);
                         }
                     } else {
-                        const uint32_t on = cm[c >> 1] >> (16 * (c & 1));
+                        const uint32_t on = (c < 2 ? cm[0] : cm[1]) >> (16 * (c & 1));
 #pragma unroll
                         for (int k = 0; k < 16; k += 2) {
                             const bool o0 = (on >> k) & 1u, o1 = (on >> (k + 1)) & 1u;
                             const float p0 = o0 ? __uint_as_float(e[k]) * f : 0.0f;
                             const float p1 = o1 ? __uint_as_float(e[k + 1]) * f : 0.0f;
                             w[k >> 1] = pack_bf16(p0, p1);
-                            ds[c * 8 + (k >> 1)] = pack_bf16(o0 ? p0 * (__uint_as_float(v[k]) - delta) : 0.0f,
-                                                             o1 ? p1 * (__uint_as_float(v[k + 1]) - delta) : 0.0f);
+                            ds[k >> 1] = pack_bf16(o0 ? p0 * (__uint_as_float(v[k]) - delta) : 0.0f,
+                                                   o1 ? p1 * (__uint_as_float(v[k + 1]) - delta) : 0.0f);
                         }
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j] = ds[c * 8 + j] = 0u;
+                    for (int j = 0; j < 8; ++j) w[j] = ds[j] = 0u;
                 }
                 *reinterpret_cast<uint4 *>(prow + (((c * 2) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 *reinterpret_cast<uint4 *>(prow + (((c * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                tmem_st8(tG + half * 64 + c * 8, ds);
             }
-            tmem_st<32>(tG + half * 64, ds);
             tmem_wait_st();
             fence_async_smem();
             tc_fence_before();
             warp_arrive(smem_u32(&sBarP[g]));
             if (ok) ok = mbar_wait(barV, par, status);
             tc_fence_after();
-            if (multi) {  // while P is still there
+            if constexpr (MULTI) {  // while P is still there
                 uint32_t ov[HALF_D];
                 tmem_ld_nowait<HALF_D>(tV + half * HALF_D, ov);
                 tmem_wait_ld();
@@ -986,10 +997,17 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
                 if (OWN && (tid & 255) == 0)
                     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sEmpty[st][1])) : "memory");
             }
+            {
+                uint32_t ds[2][16];
+                tmem_ld16_nowait(tG + half * 64, ds[0]);
+                tmem_ld16_nowait(tG + half * 64 + 16, ds[1]);
+                tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4 *>(prow + ((j ^ (r & 7)) << 4)) =
-                    make_uint4(ds[4 * j], ds[4 * j + 1], ds[4 * j + 2], ds[4 * j + 3]);
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t *x = ds[j >> 2] + 4 * (j & 3);
+                    *reinterpret_cast<uint4 *>(prow + ((j ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            }
             fence_async_smem();
             tc_fence_before();
             warp_arrive(smem_u32(&sBarD[g]));
@@ -999,7 +1017,7 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
             tmem_ld_nowait<HALF_D>(tQ + half * HALF_D, oq);
             tmem_ld_nowait<HALF_D>(tK + half * HALF_D, ok_);
             tmem_wait_ld();
-            if (multi) {
+            if constexpr (MULTI) {
                 if (group_any(g, row >= 0 && (bad(oq) || bad(ok_)))) {
                     if (row >= 0 && bad(oq)) mend(oq, false, gs0 + L::TENSOR);
                     if (row >= 0 && bad(ok_)) mend(ok_, true, gs0);
@@ -1088,8 +1106,8 @@ bt_status launch_simt(const BwdArgs &a)
     return run_simt<T, D, 256>(a);
 }
 
-template <int D>
-bt_status launch_tc(const BwdArgs &a)
+template <int D, bool MULTI>
+bt_status run_tc(const BwdArgs &a)
 {
     using L = BwdTc<D>;
     constexpr size_t smem = L::BYTES;
@@ -1098,7 +1116,7 @@ bt_status launch_tc(const BwdArgs &a)
     const int sms = device_sms(&dev);
     if (sms == 0) return BT_ERR_CUDA;
     const bt_status s = setup_once(set[dev], [&]() -> bt_status {
-        return cudaFuncSetAttribute(k_ball_bwd_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) ==
+        return cudaFuncSetAttribute(k_ball_bwd_tc<D, MULTI>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) ==
                        cudaSuccess
                    ? BT_OK
                    : BT_ERR_CUDA;
@@ -1117,11 +1135,17 @@ bt_status launch_tc(const BwdArgs &a)
     const int64_t most = L::OWN ? (items + 1) / 2 : items;  // CTAs that have work
     const unsigned grid = unsigned(most < sms ? most : sms);
     const float scale = 1.0f / sqrtf(float(D));
-    k_ball_bwd_tc<D><<<grid, BwdTc<D>::THREADS, smem, a.st>>>(
+    k_ball_bwd_tc<D, MULTI><<<grid, BwdTc<D>::THREADS, smem, a.st>>>(
         mq, mk, mv, mg, a.perm, a.npad, a.rows, a.m, spt, a.H, scale, scale * 1.4426950408889634f, int(items),
         static_cast<__nv_bfloat16 *>(a.dQ), static_cast<__nv_bfloat16 *>(a.dK), static_cast<__nv_bfloat16 *>(a.dV),
         status);
     return cudaPeekAtLastError() == cudaSuccess ? BT_OK : BT_ERR_CUDA;
+}
+
+template <int D>
+bt_status launch_tc(const BwdArgs &a)
+{
+    return a.m <= 64 ? run_tc<D, true>(a) : run_tc<D, false>(a);  // two balls or more in a tile, or one
 }
 
 }  // namespace
