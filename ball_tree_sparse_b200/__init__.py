@@ -622,7 +622,7 @@ def bt_rms_norm_backward(dY: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
         _want("dw", dw, (C,), torch.float32, dev)
         _apart("dw", dw, h, weight, dY, dH, out)
     elif weight is not None:
-        dw = _new(h, stream, (C,), torch.float32)
+        dw = _new(weight, stream)
     if out is not None:
         _want("out", out, shape, dtype, dev)
         _apart("out", out, h, weight, same=(dY, dH))
@@ -668,7 +668,10 @@ def bt_qkv_project_i8(Xq: torch.Tensor, xs: torch.Tensor, Wq: torch.Tensor, ws: 
         _want("inv", inv, (rows,), torch.int32, dev)
     shape = (npad, H, d)
     if out is None:
-        Q, K, V = _new(Xq, stream, shape, dtype), _new(Xq, stream, shape, dtype), _new(Xq, stream, shape, dtype)
+        if H * d % 8 == 0:  # each aligned to 16 bytes
+            Q, K, V = _new(Xq, stream, (3, *shape), dtype).unbind(0)
+        else:
+            Q, K, V = (_new(Xq, stream, shape, dtype) for _ in range(3))
     else:
         Q, K, V = out
         for n, t in (("Q", Q), ("K", K), ("V", V)):
