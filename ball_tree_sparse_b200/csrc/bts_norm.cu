@@ -68,8 +68,8 @@ template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float
 
 // The vectors of a row that a thread holds: vector i at column col(i) of C, `p` the row's first element; zeros where it has
 // none (or !live).  EDGE: the first and last may reach into the neighbouring rows, whose elements are read with the rest
-// (and perhaps while they are written) and dropped by mask_edge.  `end`: nothing follows the row, and single elements are
-// read where it ends inside a vector.  All loads are issued before any is used.
+// (and perhaps while they are written) and dropped by mask_edge.  `end`: less than a vector follows the row, and single
+// elements are read where it ends inside one.  All loads are issued before any is used.
 template <bool EDGE, typename T, int VEC, int NV, typename F>
 __device__ __forceinline__ void load_row(Pack<T, VEC> (&k)[NV], const T *p, int C, bool live, bool end, F &&col)
 {
@@ -187,8 +187,9 @@ __global__ void __launch_bounds__(kNormThreads)
     float h[NV * VEC];
     {
         Pack<T, VEC> k[NV], rr[NV];
-        load_row<SHIFT>(k, X + base, C, live, row == rows - 1, col);
-        if (R) load_row<SHIFT>(rr, R + base, C, live, row == rows - 1, col);
+        const bool end = SHIFT && (rows - 1 - row) * C < VEC;
+        load_row<SHIFT>(k, X + base, C, live, end, col);
+        if (R) load_row<SHIFT>(rr, R + base, C, live, end, col);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = col(i);
@@ -324,9 +325,10 @@ __global__ void __launch_bounds__(kNormThreads, (BwdShape<T, VEC, NV>::PER_SM))
     };
     auto fetch = [&](Row &k, int64_t row) {
         const size_t base = size_t(row) * C;
-        load_row<SHIFT>(k.h, H + base, C, row < rows, row == rows - 1, col);
-        load_row<SHIFT>(k.y, dY + base, C, row < rows, row == rows - 1, col);
-        if (dH) load_row<SHIFT>(k.u, dH + base, C, row < rows, row == rows - 1, col);
+        const bool end = SHIFT && (rows - 1 - row) * C < VEC;
+        load_row<SHIFT>(k.h, H + base, C, row < rows, end, col);
+        load_row<SHIFT>(k.y, dY + base, C, row < rows, end, col);
+        if (dH) load_row<SHIFT>(k.u, dH + base, C, row < rows, end, col);
     };
     Row k;
     if (PF) fetch(k, G);
