@@ -17,6 +17,7 @@
 
 #include <cfloat>
 #include <cmath>
+#include <cstring>
 
 #include "bts_internal.cuh"
 #include "bts_maps.cuh"
@@ -65,6 +66,23 @@ __device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162floa
 template <typename T> __device__ __forceinline__ T narrow(float v);
 template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Two floats in one register pair and packed instructions on them (sm_100), each half an IEEE operation.
+struct F2 {
+    unsigned long long v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ float lo() const { float a, b; asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); return a; }
+    __device__ __forceinline__ float hi() const { float a, b; asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); return b; }
+};
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) { F2 r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v)); return r; }
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) { F2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v)); return r; }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
 
 // The vectors of a row that a thread holds: vector i at column col(i) of C, `p` the row's first element; zeros where it has
 // none (or !live).  EDGE: the first and last may reach into the neighbouring rows, whose elements are read with the rest
@@ -158,7 +176,7 @@ __device__ __forceinline__ V row_reduce(V v, int tpr, V *red, int &turn, F &&joi
         V *half = red + 8 * (turn & 1);
         ++turn;
         if ((threadIdx.x & 31) == 0) half[w] = v;
-        row_barrier(w0 / nw, tpr);
+        row_barrier(w0 >> (31 - __clz(nw)), tpr);
         v = half[w0];
         for (int i = 1; i < nw; ++i) v = join(v, half[w0 + i]);
     }
@@ -174,10 +192,9 @@ __global__ void __launch_bounds__(kNormThreads)
                float eps, bool norm, T *Hout, T *Y, int8_t *Q, float *scale)
 {
     __shared__ float red[16];
-    __shared__ uint32_t redm[16];
     int turn = 0;
-    const int rpb = int(blockDim.x) / tpr, t = int(threadIdx.x) % tpr;
-    const int64_t row = int64_t(blockIdx.x) * rpb + int(threadIdx.x) / tpr;
+    const int lg = 31 - __clz(tpr), t = int(threadIdx.x) & (tpr - 1);  // tpr is a power of two
+    const int64_t row = int64_t(blockIdx.x) * (int(blockDim.x) >> lg) + (int(threadIdx.x) >> lg);
     const bool live = row < rows;  // dead groups stay for the shuffles
     const size_t base = live ? size_t(row) * C : 0;
     const int sh = SHIFT ? int(base & (VEC - 1)) : 0;
@@ -233,18 +250,19 @@ __global__ void __launch_bounds__(kNormThreads)
             }
         }
     } else {
-        // absolute values as integers have the same order, with infinities and NaN above the finite ones: such a row has
-        // scale NaN and values 0
-        uint32_t mb = 0;
+        // a value that is not finite leaves NaN in its product with 0: such a row has scale NaN and values 0
+        float mx = 0.0f, nf = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV * VEC; ++i) {
             const int c = col(i / VEC) + i % VEC;
-            const uint32_t a = __float_as_uint(h[i]) & 0x7FFFFFFFu;
-            mb = max(mb, !SHIFT || (c >= 0 && c < C) ? a : 0u);  // (0 * an infinite 1 / rms beside the row is NaN)
+            const float y = !SHIFT || unsigned(c) < unsigned(C) ? h[i] : 0.0f;  // (0 times an infinite 1 / rms is NaN too)
+            mx = fmaxf(mx, fabsf(y));
+            nf = fmaf(y, 0.0f, nf);
         }
-        mb = row_reduce(mb, tpr, redm, turn, [](uint32_t a, uint32_t b) { return max(a, b); });
-        const bool bad = mb >= 0x7F800000u;
-        const float s = bad ? nanf("") : __uint_as_float(mb) / 127.0f;
+        mx = nf == 0.0f ? mx : INFINITY;
+        mx = row_reduce(mx, tpr, red, turn, [](float a, float b) { return fmaxf(a, b); });
+        const bool bad = mx > FLT_MAX;
+        const float s = bad ? nanf("") : mx / 127.0f;
         if (live && t == 0) scale[row] = s;
         // y / s correctly rounded, from the correctly rounded reciprocal and the exact remainders of the multiply-add
         // (Markstein: from a quotient within one unit in the last place, one step gives the rounded one; the first step
@@ -258,13 +276,28 @@ __global__ void __launch_bounds__(kNormThreads)
             if (has(c)) {
                 Pack<int8_t, VEC> k;
                 if (quick) {
+                    uint32_t b[VEC];
+                    if constexpr (VEC == 1) {
+                        float q = h[i] * inv;
+                        q = fmaf(fmaf(-q, s, h[i]), inv, q);
+                        q = fmaf(fmaf(-q, s, h[i]), inv, q);
+                        k.v[0] = int8_t(__float_as_int(q + 12582912.0f));
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float y = h[i * VEC + e];
-                        float q = y * inv;
-                        q = fmaf(fmaf(-q, s, y), inv, q);
-                        q = fmaf(fmaf(-q, s, y), inv, q);
-                        k.v[e] = int8_t(__float_as_int(q + 12582912.0f));
+                        for (int e = 0; e < VEC; e += 2) {
+                            const F2 y(h[i * VEC + e], h[i * VEC + e + 1]), ns(-s, -s), in(inv, inv);
+                            F2 q = y * in;
+                            q = fma2(fma2(q, ns, y), in, q);
+                            q = fma2(fma2(q, ns, y), in, q);
+                            q = q + F2(12582912.0f, 12582912.0f);
+                            b[e] = __float_as_uint(q.lo());
+                            b[e + 1] = __float_as_uint(q.hi());
+                        }
+                        uint32_t w[VEC / 4];
+#pragma unroll
+                        for (int e = 0; e < VEC; e += 4)
+                            w[e / 4] = __byte_perm(__byte_perm(b[e], b[e + 1], 0x0040), __byte_perm(b[e + 2], b[e + 3], 0x0040), 0x5410);
+                        memcpy(&k, w, VEC);
                     }
                 } else {
 #pragma unroll
@@ -305,7 +338,7 @@ __global__ void __launch_bounds__(kNormThreads, (BwdShape<T, VEC, NV>::PER_SM))
     extern __shared__ float acc_sm[];  // [groups][C] while the block's groups are joined
     __shared__ float2 red[16];
     int turn = 0;
-    const int rpb = int(blockDim.x) / tpr, t = int(threadIdx.x) % tpr, grp = int(threadIdx.x) / tpr;
+    const int lg = 31 - __clz(tpr), rpb = int(blockDim.x) >> lg, t = int(threadIdx.x) & (tpr - 1), grp = int(threadIdx.x) >> lg;
     const int64_t step = int64_t(gridDim.x) * rpb, G = int64_t(blockIdx.x) * rpb + grp;
     const int sh = SHIFT ? int((size_t(G) * C) & (VEC - 1)) : 0;
     auto col = [&](int i) { return (i * tpr + t) * VEC - sh; };
