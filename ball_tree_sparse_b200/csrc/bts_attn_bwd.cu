@@ -54,7 +54,8 @@ __device__ __forceinline__ bool finite4(const float4 &v)
 //   B  dV += P^T dO and dK += dS^T Q: a thread keeps KPT keys x 4 columns of each over all queries.
 //   C  dQ = dS K of the 32 queries.
 // Rows are padded by 16 bytes, which keeps the 16-byte accesses of A, B and C free of bank conflicts.
-// Bound by the float pipe and shared-memory loads together (A: 40 cycles of loads to 32 of products).
+// Bound by the float pipe and shared-memory loads together (A: 40 cycles of loads to 32 of products), and by latency, as
+// one or two CTAs fit an SM: 17 to 23 TFLOP/s (65,536 rows of 8 x 32 floats in balls of 128: 1.23 ms).
 // ---------------------------------------------------------------------------
 template <int D, int MP>
 struct BwdSimt {
@@ -308,9 +309,16 @@ __global__ void __launch_bounds__(BwdSimt<D, MP>::NT)
 // P and dS take turns in one buffer, because two would leave no room for the second stage.  e lies in TMEM and not in
 // registers, which 640 threads would spill (64 values each beside dP: the spills cost 10 to 40% of the time).  For d = 32
 // the next item's S is computed while this one's dS is written.
-// A key of another ball or a dummy has P = dS = 0.  Where a tile holds several balls, a value of one ball that is not
-// finite would still reach the others as 0 * value: a result that is not finite is therefore summed again over the
-// ball's own slots (`mend`).
+// A key of another ball or a dummy has P = dS = 0.  Where a tile holds several balls (MULTI), a value of one ball that is
+// not finite would still reach the others as 0 * value: a result that is not finite is therefore summed again over the
+// ball's own slots (`mend`).  One ball to a tile (m > 64) goes without those checks, and its dummies, rows of zeros, need a
+// mask in S alone: 85 us against 97 for the layer below.
+// Measured: 65,536 rows of 8 x 32 in balls of 128, 85 us (235 MB: 2.75 TB/s; 36 us at the rate of a copy); 1,048,576 rows
+// of 4 x 32, 604 to 630 us; 70,001 rows of 5 x 64 in balls of 64, 119 us.  Two things of about the same length bound it: the
+// gathers (58 cycles per request of four rows with two warps issuing: 7,400 of an item's 9,700 cycles for d = 32) and a
+// group's chain of waits and arithmetic (5,900 cycles from a tile's arrival to P and dS, 3,800 for the last products).
+// Without any loads the layer takes 80 us, without the exponentials 80.  The loops over keys are kept rolled: unrolled,
+// the code did not fit the instruction cache, and its registers spilled (97 us).
 // ---------------------------------------------------------------------------
 template <int D>
 struct BwdTc {
@@ -324,7 +332,8 @@ struct BwdTc {
     static constexpr int GROUP = 256, THREADS = 640;
     // TMEM columns of a group: S, then e; dP, then dS (bf16 pairs) in columns 0-31 and 64-95 of it.  The results lie beside
     // dS, and dK over it; what does not fit there (d = 64) over e.
-    static constexpr uint32_t TMEM = 256, T_G = 128, T_K = T_G, T_V = D == 32 ? T_G + 32 : 0, T_Q = D == 32 ? T_G + 96 : 64;
+    static constexpr uint32_t TMEM = 256, T_G = 128, T_K = T_G, T_V = D == 32 ? T_G + 32 : 0,
+                              T_Q = D == 32 ? T_G + 96 : 64;
 };
 
 __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16])
@@ -484,8 +493,8 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
     constexpr int HALF_D = D / 2;
     constexpr uint32_t SBO = 1024, SW128 = 2, MN_A = 1u << 15;
     // descriptors but for the address, in units of 16 bytes
-    constexpr uint64_t DESC = (uint64_t(SBO >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(SW128) << 61) | (1u << 16);
-    constexpr uint64_t DESC_P = (uint64_t(SBO >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(SW128) << 61) | (uint64_t(L::BLK >> 4) << 16);
+    constexpr uint64_t DESC0 = (uint64_t(SBO >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(SW128) << 61);
+    constexpr uint64_t DESC = DESC0 | (1u << 16), DESC_P = DESC0 | (uint64_t(L::BLK >> 4) << 16);
     constexpr uint32_t IDESC_S = idesc_bf16(128, false);        // S, dP
     constexpr uint32_t IDESC_Q = idesc_bf16(D, true);           // dQ: A as it lies in TMEM
     constexpr uint32_t IDESC_T = idesc_bf16(D, true) | MN_A;    // dV, dK: A transposed
@@ -620,7 +629,8 @@ __global__ void __launch_bounds__(BwdTc<D>::THREADS, 1)
                         if (OWN && !MULTI) mma_commit(smem_u32(&sEmpty[st][1]));
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            mma_ts(tS + L::T_Q, tS + L::T_G + 64 * (kk >> 2) + 8 * (kk & 3), s0 + (L::TENSOR + 2048 * kk) / 16, DESC, IDESC_Q, kk > 0);
+                            mma_ts(tS + L::T_Q, tS + L::T_G + 64 * (kk >> 2) + 8 * (kk & 3),
+                                   s0 + (L::TENSOR + 2048 * kk) / 16, DESC, IDESC_Q, kk > 0);
                     }
                     __syncwarp();
                 }
