@@ -55,7 +55,8 @@ __device__ __forceinline__ bool finite4(const float4 &v)
 //   C  dQ = dS K of the 32 queries.
 // Rows are padded by 16 bytes, which keeps the 16-byte accesses of A, B and C free of bank conflicts.
 // Bound by the float pipe and shared-memory loads together (A: 40 cycles of loads to 32 of products), and by latency, as
-// one or two CTAs fit an SM: 17 to 23 TFLOP/s (65,536 rows of 8 x 32 floats in balls of 128: 1.23 ms).
+// one to five CTAs fit an SM: 15 to 24 TFLOP/s (65,536 rows of 8 x 32 floats in balls of 128: 0.90 ms; 1.23 without the
+// bound on registers that lets two CTAs of that shape share an SM).
 // ---------------------------------------------------------------------------
 template <int D, int MP>
 struct BwdSimt {
@@ -68,7 +69,7 @@ struct BwdSimt {
 };
 
 template <typename T, int D, int MP>
-__global__ void __launch_bounds__(BwdSimt<D, MP>::NT)
+__global__ void __launch_bounds__(BwdSimt<D, MP>::NT, D == 32 && MP == 128 ? 2 : 1)
     k_ball_bwd_simt(const T *__restrict__ Q, const T *__restrict__ K, const T *__restrict__ V,
                     const T *__restrict__ dO, const int32_t *__restrict__ perm, int64_t npad, int64_t rows, int m,
                     int spt, int H, float scale, T *__restrict__ dQ, T *__restrict__ dK, T *__restrict__ dV,

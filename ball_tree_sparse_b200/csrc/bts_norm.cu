@@ -14,7 +14,7 @@
 // into its first vector, and the first and last vectors are read and written by element.  All tensors of a call have the
 // same shape, so they share the shift.  Only where an address is not aligned is VEC 1.
 // Measured (bf16): 1,048,576 x 128 with residual 170 us, 98% of a copy's rate; 65,536 x 256 with residual 26 us (79%);
-// 1,048,576 x 128 with residual to 8 bits 195 us (75%: arithmetic); backward, 1,048,576 x 128 189 us (88%), 65,536 x 256
+// 1,048,576 x 128 with residual to 8 bits 176 us (83%: arithmetic); backward, 1,048,576 x 128 189 us (88%), 65,536 x 256
 // 32 us (64%); odd lengths are bound by the instructions for their edges (100,000 x 333: 115 us, 36%).
 #include <cuda_bf16.h>
 
@@ -203,8 +203,11 @@ __device__ __forceinline__ V row_reduce(V v, int tpr, V *red, int &turn, F &&joi
 // One row per group of tpr threads.  I8: q and scale instead of Y.  norm == false: y = h (quantisation alone).
 // X, R and Hout may be the same tensor: a thread reads its elements before it writes them, so these loads are
 // plain ones.  SHIFT: C is no multiple of VEC.
+// Three blocks of 256 threads to an SM where a thread holds 32 elements: two, which the registers would make, leave
+// 1,048,576 x 128 bf16 to 8 bits at 217 us instead of 176, and four spill (197).  With a shift the bound spills (30,000 x
+// 1,777 floats: 250 us instead of 180).
 template <typename T, int VEC, int NV, bool SHIFT, bool I8>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, NV * VEC == 32 && !SHIFT ? 3 : 0)
     k_rms_norm(const T *X, const T *R, const float *__restrict__ w, int64_t rows, int C, float invC, int tpr,
                float eps, bool norm, T *Hout, T *Y, int8_t *Q, float *scale)
 {
@@ -467,9 +470,8 @@ struct NormShape {
 // 16-byte vectors where the addresses are aligned (and the weight's, where the vectors follow its own), else single
 // elements.  Then the threads of a row:
 //   forward   as few as hold it in 32 / VEC vectors each, but four that share 64 bytes (a row per thread reads bytes far
-//             apart), when there are rows enough to fill the SMs; else as many as the row has vectors.  In 8 bits 16 / VEC
-//             where a warp is enough for that: there more of a row's time is arithmetic, and more threads hide it
-//             (1,048,576 x 128 bf16: 266 -> 205 us, but 170 -> 185 us with 16 bits out).
+//             apart), when there are rows enough to fill the SMs; else as many as the row has vectors.  In 8 bits with
+//             a shift 16 / VEC where a warp is enough for that (100,000 x 333 bf16: 127 us, 143 with 32 / VEC).
 //   backward  a vector each, or two of floats, up to 256 threads: a thread keeps its part of the weight and of dw.
 template <typename T>
 NormShape norm_shape(int64_t rows, int C, uintptr_t al, uintptr_t al_q, uintptr_t al_w, bool backward,
@@ -489,7 +491,7 @@ NormShape norm_shape(int64_t rows, int C, uintptr_t al, uintptr_t al_q, uintptr_
     if (backward) {
         while (tpr * (sizeof(T) == 4 ? 2 : 1) < cv && tpr < kNormThreads) tpr <<= 1;
     } else {
-        while ((i8 && tpr * most / 2 < cv && tpr < 32) || tpr * most < cv || (tpr < 4 && tpr < cv)) tpr <<= 1;
+        while ((i8 && s.shift && tpr * most / 2 < cv && tpr < 32) || tpr * most < cv || (tpr < 4 && tpr < cv)) tpr <<= 1;
         // few rows: spread each over more threads, down to one vector each
         while (tpr < cv && tpr < kNormThreads && rows * tpr < 148 * 512) tpr <<= 1;
     }
