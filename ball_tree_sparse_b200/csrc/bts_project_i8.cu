@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(256)
 // Tensor cores (tcgen05.mma kind::i8, 32-bit integer sums in TMEM).  A CTA keeps to one chunk of BN output channels and
 // walks the 128-row tiles of X:
 //   warps 17-20  loaders.  TMA: one thread fetches 128 x 128-byte boxes (128-byte swizzle; rows and columns outside read
-//               zeros).  Otherwise (row lengths or addresses that no tensor map takes) the four warps copy 16 bytes a
-//               thread, put together from aligned words.
+//               zeros).  Otherwise (row lengths or addresses that no tensor map takes) the four warps copy rows, put
+//               together from aligned words.
 //   warp 16      issues the products, two accumulators of BN columns;
 //   warps 0-15   four warps per 32 rows, a quarter of the columns (but at least 32) each: scale, round, pass through
 //                4 KB of shared memory of the warp's own, and store 128-byte pieces of rows to the row's slot of Q, K
@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(256)
 // W stays in shared memory where the chunk's rows fit (`keep`), else it is fetched with each block of X.
 // Bound by the integer products: 65,536 x 256 -> 768 keeps the tensor pipe active for 23 us (4,096 operations a cycle and
 // SM, half of what bf16 has); its 118 MB take 18 us.  Measured: 39 us; the rest is the launch, W's arrival, and eleven
-// tiles a CTA where 10.4 are due.  Eight storing warps instead of sixteen: 43.
+// tiles a CTA where 10.4 are due.  Eight storing warps instead of sixteen: 43.  Without TMA the copying warps bound it
+// (65,536 x 255: 114 us).
 // ---------------------------------------------------------------------------
 struct I8Tile {
     static constexpr int BM = 128, BK = 128, EPI = 16, THREADS = (EPI + 5) * 32;
@@ -242,42 +243,50 @@ __device__ __forceinline__ void mma_i8(uint32_t tmem_d, uint64_t a, uint64_t b, 
         : "memory");
 }
 
-// 16 bytes of row `r` at column c (a multiple of 16) of the [n][C] bytes at M, zeros outside; no alignment needed.
-__device__ __forceinline__ uint4 bytes16(const int8_t *__restrict__ M, int64_t n, int C, int64_t r, int c)
+// The aligned word at p of a matrix that begins and ends at the given addresses; a word that reaches out of it comes byte by
+// byte, with zeros outside.
+__device__ __forceinline__ uint32_t word_at(uintptr_t p, uintptr_t begin, uintptr_t end)
 {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    const int left = min(16, C - c);
-    if (r >= n || left <= 0) return v;
-    const int8_t *p = M + size_t(r) * C + c;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    const uintptr_t end = reinterpret_cast<uintptr_t>(M) + size_t(n) * C;  // words past it are put together from bytes
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(a & ~uintptr_t(3));
-    const int sh = int(a & 3) * 8;
-    uint32_t x[5];
+    if (p >= begin && p + 4 <= end) return __ldg(reinterpret_cast<const uint32_t *>(p));
+    uint32_t x = 0;
 #pragma unroll
-    for (int i = 0; i < 5; ++i) {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(w + i);
-        x[i] = 0;
-        if (at >= a + left) continue;
-        if (at >= reinterpret_cast<uintptr_t>(M) && at + 4 <= end) {
-            x[i] = __ldg(w + i);
+    for (int b = 0; b < 4; ++b)
+        if (p + b >= begin && p + b < end) x |= uint32_t(uint8_t(__ldg(reinterpret_cast<const int8_t *>(p + b)))) << (8 * b);
+    return x;
+}
+
+// Columns c0 .. c0 + 127 of row r of the [n][C] bytes at M by a warp: lane l gets bytes 4l .. 4l + 3, zeros outside.  No
+// alignment needed: neighbouring lanes read neighbouring words, and each shifts its own and the next lane's together.
+struct RowWords {
+    uint32_t x, last;
+    int left, sh;
+    // INSIDE: no word of the row reaches out of the matrix, and the loads wait for nothing
+    template <bool INSIDE>
+    __device__ __forceinline__ void load(const int8_t *__restrict__ M, int64_t n, int C, int64_t r, int c0, int lane)
+    {
+        const uintptr_t begin = reinterpret_cast<uintptr_t>(M), end = begin + size_t(n) * C;
+        const uintptr_t a = begin + size_t(r) * C + c0, w = a & ~uintptr_t(3);
+        left = r < n ? min(128, C - c0) : 0;
+        sh = int(a & 3) * 8;
+        const int words = left ? (int(a & 3) + left + 3) >> 2 : 0;  // up to 33
+        x = last = 0u;
+        if constexpr (INSIDE) {
+            if (lane < words) x = __ldg(reinterpret_cast<const uint32_t *>(w) + lane);
+            if (lane == 31 && words > 32) last = __ldg(reinterpret_cast<const uint32_t *>(w) + 32);
         } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (at + b >= a && at + b < a + left)
-                    x[i] |= uint32_t(uint8_t(__ldg(reinterpret_cast<const int8_t *>(at + b)))) << (8 * b);
+            if (lane < words) x = word_at(w + 4 * lane, begin, end);
+            if (lane == 31 && words > 32) last = word_at(w + 128, begin, end);
         }
     }
-    uint32_t y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        y[i] = __funnelshift_r(x[i], x[i + 1], sh);
-        const int rest = left - 4 * i;  // bytes of this word inside the row
-        if (rest <= 0) y[i] = 0;
-        else if (rest < 4) y[i] &= (1u << (8 * rest)) - 1u;
+    __device__ __forceinline__ uint32_t get(int lane) const
+    {
+        uint32_t next = __shfl_down_sync(0xffffffffu, x, 1);
+        next = lane == 31 ? last : next;
+        const uint32_t y = __funnelshift_r(x, next, sh);
+        const int rest = left - 4 * lane;  // bytes of this word inside the row
+        return rest >= 4 ? y : rest <= 0 ? 0u : y & ((1u << (8 * rest)) - 1u);
     }
-    return make_uint4(y[0], y[1], y[2], y[3]);
-}
+};
 
 template <typename T, int BN, bool TMA>
 __global__ void __launch_bounds__(I8Tile::THREADS, 1)
@@ -363,13 +372,25 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
                     mbar_wait(smem_u32(&sFull[k % stages]), (k / stages) & 1, status);
             }
         } else {
-            const int lt = tid - (L::EPI + 1) * 32;  // 0 .. 127
+            const int lw = warp - L::EPI - 1;  // 0 .. 3: every fourth row
             auto block = [&](const int8_t *M, int64_t n, int64_t r0, int nr, int k, uint32_t off) {
-#pragma unroll 4
-                for (int u = lt; u < nr * 8; u += 128) {
-                    const int r = u >> 3, c = u & 7;
-                    const uint4 v = bytes16(M, n, C, r0 + r, k * L::BK + c * 16);
-                    *reinterpret_cast<uint4 *>(gbase + off + r * 128 + ((c ^ (r & 7)) << 4)) = v;
+                const bool inside = r0 > 0 && r0 + nr < n && C >= 4;  // a word at least before and after the rows
+#pragma unroll 1
+                for (int r1 = lw; r1 < nr; r1 += 32) {  // eight rows under way at a time: sixteen spill
+                    RowWords v[8];
+                    if (inside) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i].load<true>(M, n, C, r0 + r1 + 4 * i, k * L::BK, lane);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i].load<false>(M, n, C, r0 + r1 + 4 * i, k * L::BK, lane);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r1 + 4 * i;
+                        *reinterpret_cast<uint32_t *>(gbase + off + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
+                                                      (lane & 3) * 4) = v[i].get(lane);
+                    }
                 }
             };
             auto arrive = [&](uint64_t *bar) {
