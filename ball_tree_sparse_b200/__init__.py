@@ -673,7 +673,7 @@ def bt_qkv_project_i8(Xq: torch.Tensor, xs: torch.Tensor, Wq: torch.Tensor, ws: 
     if perm is None:
         inv = None
     elif inv is None:
-        inv = bt_invert_perm(perm, rows, stream=stream)
+        inv = bt_invert_perm(perm, rows, _array((rows,), torch.int32, dev, stream), stream)
     else:
         _want("inv", inv, (rows,), torch.int32, dev)
     shape = (npad, H, d)

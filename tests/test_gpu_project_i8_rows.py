@@ -57,3 +57,27 @@ def test_many_tiles_in_tree_order():
             assert (a[perm < 0] == 0).all()
         want = plain64.project_i8(x[:500], xs[:500], w, ws)[:, :H * d].reshape(500, H, d)
         plain64.within(plain[0][:500], want, 1.01 * (3 * U + HALF[BF16]) * want.abs() + 1e-38)
+
+
+def test_what_a_call_allocates_belongs_to_its_stream():
+    # the inverse of perm that the call makes is given back to the stream that uses it: an array that the current stream
+    # allocates while the work is still to come must not share its memory
+    rows, C, H, d = 1 << 20, 16, 1, 8
+    (x, xs), (w, ws) = _inside(rows, C, 0, 1), _inside(3 * H * d, C, 0, 2)
+    perm = torch.arange(rows, dtype=torch.int32, device="cuda")
+    want = bts.bt_qkv_project_i8(x, xs, w, ws, H, d, perm=perm)
+    side = torch.cuda.Stream()
+
+    def fill():
+        return [torch.full((rows,), 7, dtype=torch.int32, device="cuda") for _ in range(16)]
+    bts.bt_qkv_project_i8(x, xs, w, ws, H, d, perm=perm, stream=side)  # so that nothing below asks the driver for memory
+    fill()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    got = bts.bt_qkv_project_i8(x, xs, w, ws, H, d, perm=perm, stream=side)
+    mine = fill()
+    assert not side.query()  # the work is still to come
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in mine)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
