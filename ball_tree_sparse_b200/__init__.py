@@ -670,7 +670,7 @@ def bt_qkv_project_i8(Xq: torch.Tensor, xs: torch.Tensor, Wq: torch.Tensor, ws: 
     _want("ws", ws, (3 * H * d,), torch.float32, dev)
     npad = _slots(perm, None, rows, dev)
     st = _handle(dev, stream)
-    if perm is None:
+    if perm is None or npad == 0:
         inv = None
     elif inv is None:
         inv = bt_invert_perm(perm, rows, _array((rows,), torch.int32, dev, stream), stream)
@@ -689,6 +689,8 @@ def bt_qkv_project_i8(Xq: torch.Tensor, xs: torch.Tensor, Wq: torch.Tensor, ws: 
             _apart(n, t, Xq, xs, Wq, ws, perm, inv, *(u for u in (Q, K, V) if u is not t))
         if Q is K or Q is V or K is V:
             raise ValueError("Q, K and V may not share memory")
+    if npad == 0:  # no slot to write (and an empty perm has no address to tell it from none)
+        return Q, K, V
     _check("bt_qkv_project_i8",
            _lib.bt_qkv_project_i8(_at(Xq), _at(xs), rows, C, _at(Wq), _at(ws), H, d,
                                   BT_F32 if dtype == torch.float32 else BT_BF16, _at(perm), _at(inv), npad, _at(Q),

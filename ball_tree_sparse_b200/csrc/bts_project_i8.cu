@@ -695,7 +695,8 @@ extern "C" size_t bt_projected_i8_workspace_size(int64_t npad, int64_t rows, int
     if (npad < 0 || rows < 0 || npad > 0x7FFFFFFF || rows > 0x7FFFFFFF || C < 1 || H < 1 || d < 1 ||
         (dt != BT_F32 && dt != BT_BF16))
         return 0;
-    return LayerWs(npad, rows, C, int64_t(H) * d, dt).total;
+    const size_t n = LayerWs(npad, rows, C, int64_t(H) * d, dt).total;
+    return n ? n : 256;  // 0 says that the sizes are refused; an empty batch is none of those
 }
 
 extern "C" bt_status bt_projected_ball_attention_i8(const void *X, const void *R, const float *gamma, float eps,

@@ -103,3 +103,9 @@ def test_layer_i8(b):
     assert call(work=None) == WORKSPACE and call(nb=n - 1) == WORKSPACE and call(work=ctypes.c_void_p(272)) == ARG
     assert call(C=8193, nb=1 << 40) == UNSUPPORTED and call(H=700, nb=1 << 40) == UNSUPPORTED
     assert call(rows=0) == 0
+
+
+def test_layer_i8_of_no_rows(b):
+    # an empty batch is served: its workspace has a size, which tells it from a refusal
+    assert b._lib.bt_projected_i8_workspace_size(0, 0, 64, 8, 32, BF16) > 0
+    assert b._lib.bt_projected_i8_workspace_size(0, 0, 64, 0, 32, BF16) == 0

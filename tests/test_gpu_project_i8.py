@@ -259,3 +259,23 @@ def test_refusals():
     with pytest.raises(bts.BtsError) as e:
         bts.bt_projected_ball_attention_i8(xf, perm, *w, 48, 2, 32, weight=gamma)
     assert e.value.status == "BT_ERR_SHAPE"
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_no_rows(dtype):
+    # an empty batch: every call returns results of no rows, the gradient of the weight is zero
+    x, r = (torch.empty((0, 64), dtype=dtype, device="cuda") for _ in range(2))
+    w8, ws = bts.bt_quantize_i8(torch.ones((192, 64), dtype=dtype, device="cuda"))
+    weight = torch.ones(64, device="cuda")
+    y, h = bts.bt_rms_norm(x, weight, r)
+    xq, xs, _ = bts.bt_rms_norm_i8(x, weight, r)
+    dx, dw = bts.bt_rms_norm_backward(y, h, weight)
+    assert y.shape == h.shape == xq.shape == dx.shape == (0, 64) and xs.shape == (0,) and (dw == 0).all()
+    for perm in (None, torch.empty(0, dtype=torch.int32, device="cuda")):
+        q, k, v = bts.bt_qkv_project_i8(xq, xs, w8, ws, 2, 32, dtype, perm)
+        assert q.shape == k.shape == v.shape == (0, 2, 32)
+        assert all(g.shape == q.shape for g in bts.bt_ball_attention_backward(q, k, v, q, perm, 16))
+        o, h = bts.bt_projected_ball_attention_i8(x, perm, w8, ws, 16, 2, 32, weight, r)
+        assert o.shape == (0, 2, 32) and h.shape == (0, 64)
+    torch.cuda.synchronize()
+    assert bts.bt_last_device_status() == 0
