@@ -196,9 +196,10 @@ __global__ void __launch_bounds__(BwdSimt<D, MP>::NT, D == 32 && MP == 128 ? 2 :
                 const float delta = dl * inv;
 #pragma unroll
                 for (int j = 0; j < L::CPL; ++j) {
-                    const float p = s[i][j] * inv;
+                    const bool on = (ok >> j) & 1u;
+                    const float p = on ? s[i][j] * inv : 0.0f;  // (inv is NaN where the row's scores left float's range)
                     sP[ri * LP + lane + 32 * j] = p;
-                    sS[ri * LP + lane + 32 * j] = (ok >> j) & 1u ? p * (g[i][j] - delta) : 0.0f;
+                    sS[ri * LP + lane + 32 * j] = on ? p * (g[i][j] - delta) : 0.0f;
                 }
             }
         }
