@@ -212,6 +212,16 @@ def bt_invert_perm(perm: torch.Tensor, n_rows: int, inv: torch.Tensor | None = N
     return inv
 
 
+BT_NO_SLOT = -2139062144  # entry of an inverse for a row that no slot names
+
+
+def _inverse(perm, rows, inv, stream):
+    """The inverse of perm in `inv`, BT_NO_SLOT for rows that no slot names."""
+    with torch.cuda.stream(stream):
+        inv.fill_(BT_NO_SLOT)
+    return bt_invert_perm(perm, rows, inv, stream)
+
+
 def bt_compose(invA: torch.Tensor, permB: torch.Tensor, out: torch.Tensor | None = None, stream=None):
     if out is None:
         out = torch.empty_like(permB)
@@ -328,12 +338,12 @@ def bt_coarse_ball_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, 
 def bt_qkv_project(X: torch.Tensor, Wt: torch.Tensor, H: int, d: int, perm: torch.Tensor | None = None,
                    inv: torch.Tensor | None = None, out=None, stream=None):
     """Q, K, V = X Wt^T.  X [rows, C] original order; Wt [3*H*d, C].  With perm (slot -> row) the outputs are
-    [npad, H, d] in slot order (row r at slot inv[r]; zeros for dummy slots) and inv is computed when not given;
-    without, [rows, H, d] in the original order."""
+    [npad, H, d] in slot order (row r at slot inv[r]; zeros for dummy slots) and inv is computed when not given
+    (rows that no slot names are stored nowhere); without, [rows, H, d] in the original order."""
     rows, C = X.shape
     npad = perm.numel() if perm is not None else rows
     if perm is not None and inv is None:
-        inv = bt_invert_perm(perm, rows, stream=stream)
+        inv = _inverse(perm, rows, torch.empty(rows, dtype=torch.int32, device=perm.device), stream)
     if out is None:
         out = tuple(torch.empty((npad, H, d), dtype=X.dtype, device=X.device) for _ in range(3))
     Q, K, V = out
@@ -659,7 +669,8 @@ def bt_qkv_project_i8(Xq: torch.Tensor, xs: torch.Tensor, Wq: torch.Tensor, ws: 
                       dtype: torch.dtype = torch.bfloat16, perm: torch.Tensor | None = None,
                       inv: torch.Tensor | None = None, out=None, stream=None):
     """Q, K, V = (Xq * xs[:, None]) (Wq * ws[:, None])^T from 8-bit integers: Xq int8 [rows, C], xs float32 [rows];
-    Wq int8 [3*H*d, C], ws float32 [3*H*d].  perm, inv and the layout of the results as for bt_qkv_project."""
+    Wq int8 [3*H*d, C], ws float32 [3*H*d].  perm, inv and the layout of the results as for bt_qkv_project (rows
+    that no slot names are stored nowhere)."""
     rows, C = Xq.shape
     dev = Xq.device
     if dtype not in (torch.float32, torch.bfloat16):
@@ -673,7 +684,7 @@ def bt_qkv_project_i8(Xq: torch.Tensor, xs: torch.Tensor, Wq: torch.Tensor, ws: 
     if perm is None or npad == 0:
         inv = None
     elif inv is None:
-        inv = bt_invert_perm(perm, rows, _array((rows,), torch.int32, dev, stream), stream)
+        inv = _inverse(perm, rows, _array((rows,), torch.int32, dev, stream), stream)
     else:
         _want("inv", inv, (rows,), torch.int32, dev)
     shape = (npad, H, d)

@@ -1009,7 +1009,11 @@ extern "C" bt_status bt_projected_ball_attention(const void *X, const int32_t *p
     int32_t *inv = reinterpret_cast<int32_t *>(w + 3 * one);
     if (perm && pair_shape(m, H, d, dt, rows) && npad >= 128) {
         // Q, K, V written in slot order (each feature row to its slot); the attention then loads every ball as one
-        // tile.  Every row must be named by a slot, as in a tree built over these rows.
+        // tile.  The workspace may hold another call's inverse: a row that no slot names must not be taken for one of
+        // its slots.
+        if (rows > npad) return BT_ERR_ARG;
+        if (cudaMemsetAsync(inv, 0x80, size_t(rows) * 4, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return BT_ERR_CUDA;
         bt_status s = bt_invert_perm(perm, npad, rows, inv, stream);
         if (s != BT_OK) return s;
         s = bt_qkv_project(X, rows, C, Wt, H, d, dt, perm, inv, npad, Q, K, V, stream);

@@ -44,8 +44,8 @@ struct ProjPipe {
 
 // Weight-stationary: CTA b owns output chunk b % nch (bn columns of Wt, loaded once into shared memory) and
 // walks the 128-row tiles b / nch, b / nch + groups, ...  inv != NULL: feature row r goes to row inv[r] of
-// Q/K/V (slot order; a slot outside [0, npad) is skipped and recorded as BT_ERR_INTERNAL); inv == NULL: to
-// row r (original order).
+// Q/K/V (slot order; BT_NO_SLOT is skipped, any other slot outside [0, npad) is skipped and recorded as
+// BT_ERR_INTERNAL); inv == NULL: to row r (original order).
 template <int BN>
 __global__ void __launch_bounds__(ProjPipe::THREADS, 1)
     k_qkv_project(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(ProjPipe::THREADS, 1)
             if (row < rows) {
                 orow = inv ? __ldg(inv + row) : int32_t(row);
                 if (inv && (orow < 0 || orow >= npad)) {  // not a slot: never write it
-                    if (half == 0) record_error(status, BT_ERR_INTERNAL);
+                    if (orow != BT_NO_SLOT && half == 0) record_error(status, BT_ERR_INTERNAL);
                     orow = -1;
                 }
             }
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(128) k_qkv_project_simt(const T *__restrict__ 
         if (row < rows) {
             o = inv ? inv[row] : int32_t(row);
             if (inv && (o < 0 || o >= npad)) {
-                if (blockIdx.y == 0) record_error(status, BT_ERR_INTERNAL);
+                if (o != BT_NO_SLOT && blockIdx.y == 0) record_error(status, BT_ERR_INTERNAL);
                 o = -1;
             }
         }

@@ -37,13 +37,14 @@ struct QkvOut {
     }
 };
 
-// The output row of feature row r, or -1 (recorded) where inv names no slot.
+// The output row of feature row r, or -1 where it has no slot; an inv entry that is neither a slot nor says so is
+// recorded.
 __device__ __forceinline__ int32_t out_row(const int32_t *inv, int64_t r, int64_t npad, uint32_t *status)
 {
     if (!inv) return int32_t(r);
     const int32_t o = __ldg(inv + r);
     if (o >= 0 && o < npad) return o;
-    record_error(status, BT_ERR_INTERNAL);
+    if (o != BT_NO_SLOT) record_error(status, BT_ERR_INTERNAL);
     return -1;
 }
 
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
                 xr = __ldg(xs + row);
                 orow = inv ? __ldg(inv + row) : int32_t(row);
                 if (inv && (orow < 0 || orow >= npad)) {  // not a slot: never write it
-                    if (quarter == 0 && chunk == 0) record_error(status, BT_ERR_INTERNAL);
+                    if (orow != BT_NO_SLOT && quarter == 0 && chunk == 0) record_error(status, BT_ERR_INTERNAL);
                     orow = -1;
                 }
             }
@@ -730,6 +731,9 @@ extern "C" bt_status bt_projected_ball_attention_i8(const void *X, const void *R
     const bool tree = perm && dt == BT_BF16 && d == 32 && H % 2 == 0 && npad >= 128 && rows < 0x7FFFFFFF &&
                       (m == 16 || m == 32 || m == 64 || m == 128);
     if (tree) {
+        // the workspace may hold another call's inverse: a row that no slot names must not be taken for one of its slots
+        if (cudaMemsetAsync(inv, 0x80, size_t(rows) * 4, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return BT_ERR_CUDA;
         s = bt_invert_perm(perm, npad, rows, inv, stream);
         if (s != BT_OK) return s;
         s = bt_qkv_project_i8(xq, xs, rows, C, Wq, ws, H, d, dt, perm, inv, npad, q, k, v, stream);

@@ -69,6 +69,9 @@ typedef enum {
 
 typedef enum { BT_F32 = 0, BT_BF16 = 1 } bt_dtype;
 
+/* Entry of an inverse slot map (inv) for a row that no slot names.  Its bytes are equal: cudaMemset(inv, 0x80, ...) */
+#define BT_NO_SLOT (-2139062144)
+
 /* Largest batch (number of clouds) one segmented build accepts. */
 #define BT_MAX_CLOUDS 64
 
@@ -184,6 +187,8 @@ bt_status bt_rotate_z(const float *in, int64_t N, float *out, void *stream);
  *   perm    int32 [npad] (dummies -1); its real slots must hold every row
  *           0..n_rows-1 exactly once (as bt_build* produces)
  *   inv     int32 [n_rows] out
+ * Only the entries of the rows that slots name are written.  Where some row may
+ * have no slot, fill inv with BT_NO_SLOT first.
  */
 bt_status bt_invert_perm(const int32_t *perm, int64_t npad, int64_t n_rows, int32_t *inv, void *stream);
 
@@ -255,8 +260,9 @@ bt_status bt_ball_attention(const void *Q, const void *K, const void *V, const i
  *   perm     int32 [npad] device (slot -> row, -1 dummy) or NULL.  Given
  *            perm, Q, K, V are [npad, H, d] in slot order and the rows of the
  *            dummy slots are set to zero; inv (int32 [rows] device, inv[r] =
- *            the slot of row r, as bt_invert_perm writes it) is required.  An
- *            inv entry outside [0, npad) is skipped and recorded as
+ *            the slot of row r, as bt_invert_perm writes it) is required.  A
+ *            row whose inv entry is BT_NO_SLOT is stored nowhere; any other
+ *            entry outside [0, npad) is skipped and recorded as
  *            BT_ERR_INTERNAL.  NULL: Q, K, V are [rows, H, d] (inv, npad unused).
  *   Q, K, V  dt device out
  * The feature rows are read in their own order as whole tiles; each output
@@ -293,8 +299,7 @@ bt_status bt_ball_attention_tree(const void *Qt, const void *Kt, const void *Vt,
  * m and d as for bt_ball_attention.
  *   ws  workspace of bt_projected_workspace_size(npad, rows, H, d, dt) bytes,
  *       256-byte aligned (the projected Q, K and V, and the inverse of perm)
- * With perm, every row must be named by a slot (as in a tree built over the
- * rows); the slot-order path relies on it.
+ * Rows that no slot names take no part, and their rows of O are left untouched.
  */
 size_t bt_projected_workspace_size(int64_t npad, int64_t rows, int32_t H, int32_t d, bt_dtype dt);
 
@@ -509,7 +514,8 @@ bt_status bt_qkv_project_i8(const int8_t *Xq, const float *xs, int64_t rows, int
  *   work  workspace of bt_projected_i8_workspace_size(npad, rows, C, H, d, dt)
  *         bytes, 256-byte aligned (the 8-bit rows and scales, Q, K, V and the
  *         inverse of perm)
- * With perm, every row must be named by a slot, as in a tree over the rows.
+ * Rows that no slot names are normed (Hout) but take no part in the attention;
+ * their rows of O are left untouched.
  */
 size_t bt_projected_i8_workspace_size(int64_t npad, int64_t rows, int32_t C, int32_t H, int32_t d, bt_dtype dt);
 
