@@ -243,14 +243,17 @@ __global__ void __launch_bounds__(128) k_qkv_project_simt(const T *__restrict__ 
     }
 }
 
-// Zero rows of Q, K and V for every dummy slot (perm < 0): one thread per slot, which writes the slot's three
-// rows (row_units units of U each) only if the slot is a dummy.
+// Zero rows of Q, K and V for every dummy slot (perm < 0, or recorded: no row of the tensors): one thread per slot,
+// which writes the slot's three rows (row_units units of U each) only if the slot is a dummy.
 template <typename U>
-__global__ void __launch_bounds__(256) k_zero_slots(const int32_t *__restrict__ perm, int64_t npad, int row_units,
-                                                    U *__restrict__ Q, U *__restrict__ K, U *__restrict__ V)
+__global__ void __launch_bounds__(256) k_zero_slots(const int32_t *__restrict__ perm, int64_t npad, int64_t rows,
+                                                    int row_units, U *__restrict__ Q, U *__restrict__ K,
+                                                    U *__restrict__ V, uint32_t *status)
 {
     for (int64_t s = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; s < npad; s += int64_t(gridDim.x) * blockDim.x) {
-        if (perm[s] >= 0) continue;
+        const int32_t r = perm[s];
+        if (r >= rows) record_error(status, BT_ERR_INTERNAL);
+        else if (r >= 0) continue;
         const size_t o = size_t(s) * row_units;
         for (int u = 0; u < row_units; ++u) {
             Q[o + u] = U{};
@@ -275,12 +278,12 @@ static bt_status launch_project(const void *X, int64_t rows, int32_t C, const vo
                              reinterpret_cast<uintptr_t>(V);
         if (row_bytes % 16 == 0 && qa % 16 == 0)
             k_zero_slots<uint4><<<unsigned(g > 0 ? g : 1), 256, 0, st>>>(
-                perm, npad, int(row_bytes / 16), static_cast<uint4 *>(Q), static_cast<uint4 *>(K),
-                static_cast<uint4 *>(V));
+                perm, npad, rows, int(row_bytes / 16), static_cast<uint4 *>(Q), static_cast<uint4 *>(K),
+                static_cast<uint4 *>(V), status);
         else
             k_zero_slots<uint16_t><<<unsigned(g > 0 ? g : 1), 256, 0, st>>>(
-                perm, npad, int(row_bytes / 2), static_cast<uint16_t *>(Q), static_cast<uint16_t *>(K),
-                static_cast<uint16_t *>(V));
+                perm, npad, rows, int(row_bytes / 2), static_cast<uint16_t *>(Q), static_cast<uint16_t *>(K),
+                static_cast<uint16_t *>(V), status);
     }
     if (rows == 0) return cudaPeekAtLastError() == cudaSuccess ? BT_OK : BT_ERR_CUDA;
     const uintptr_t al = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(Wt) |

@@ -48,11 +48,11 @@ __device__ __forceinline__ int32_t out_row(const int32_t *inv, int64_t r, int64_
     return -1;
 }
 
-// Zero rows of Q, K and V in the dummy slots (perm < 0), which no feature row fills: warp w of nw takes runs of
-// 32 slots, and all lanes write each dummy's row.
+// Zero rows of Q, K and V in the dummy slots (perm < 0, or recorded: no row of the tensors), which no feature row fills:
+// warp w of nw takes runs of 32 slots, and all lanes write each dummy's row.
 template <typename T>
-__device__ __forceinline__ void zero_dummies(const int32_t *__restrict__ perm, int64_t npad, const QkvOut<T> &out,
-                                             int64_t w, int64_t nw)
+__device__ __forceinline__ void zero_dummies(const int32_t *__restrict__ perm, int64_t npad, int64_t rows,
+                                             const QkvOut<T> &out, int64_t w, int64_t nw, uint32_t *status)
 {
     const int lane = threadIdx.x & 31;
     const int bytes = out.hd * int(sizeof(T));
@@ -60,7 +60,10 @@ __device__ __forceinline__ void zero_dummies(const int32_t *__restrict__ perm, i
                          reinterpret_cast<uintptr_t>(out.v) | uintptr_t(bytes);
     for (int64_t s0 = w * 32; s0 < npad; s0 += nw * 32) {
         const int64_t s = s0 + lane;
-        uint32_t dead = __ballot_sync(0xffffffffu, s < npad && __ldg(perm + s) < 0);
+        const int32_t r = s < npad ? __ldg(perm + s) : 0;
+        const bool none = s < npad && r >= rows;
+        if (none) record_error(status, BT_ERR_INTERNAL);
+        uint32_t dead = __ballot_sync(0xffffffffu, r < 0 || none);
         while (dead) {
             const int64_t slot = s0 + __ffs(int(dead)) - 1;
             dead &= dead - 1;
@@ -143,8 +146,8 @@ __global__ void __launch_bounds__(kFewWarps * 32)
         }
     }
     if (perm)
-        zero_dummies(perm, npad, out, int64_t(blockIdx.x) * kFewWarps + (threadIdx.x >> 5),
-                     int64_t(gridDim.x) * kFewWarps);
+        zero_dummies(perm, npad, rows, out, int64_t(blockIdx.x) * kFewWarps + (threadIdx.x >> 5),
+                     int64_t(gridDim.x) * kFewWarps, status);
 }
 
 constexpr int kTile = 64, kTileK = 64;  // rows and channels of a tile; bytes of the row length per step
@@ -208,7 +211,7 @@ __global__ void __launch_bounds__(256)
         }
     }
     if (perm && blockIdx.y == 0)
-        zero_dummies(perm, npad, out, int64_t(blockIdx.x) * 8 + (tid >> 5), int64_t(gridDim.x) * 8);
+        zero_dummies(perm, npad, rows, out, int64_t(blockIdx.x) * 8 + (tid >> 5), int64_t(gridDim.x) * 8, status);
 }
 
 // ---------------------------------------------------------------------------
@@ -347,7 +350,8 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
     if (warp > L::EPI) {
         if (TMA) {
             if (perm && warp > L::EPI + 1)  // these three have nothing to load
-                zero_dummies(perm, npad, out, int64_t(blockIdx.x) * 3 + warp - L::EPI - 2, int64_t(gridDim.x) * 3);
+                zero_dummies(perm, npad, rows, out, int64_t(blockIdx.x) * 3 + warp - L::EPI - 2, int64_t(gridDim.x) * 3,
+                             status);
             if (warp == L::EPI + 1 && lane == 0) {
                 bool ok = true;
                 if (keep) {
@@ -530,7 +534,8 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
             __syncwarp();
             if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sAccEmpty[ab])) : "memory");
         }
-        if (!TMA && perm) zero_dummies(perm, npad, out, int64_t(blockIdx.x) * L::EPI + warp, int64_t(gridDim.x) * L::EPI);
+        if (!TMA && perm)
+            zero_dummies(perm, npad, rows, out, int64_t(blockIdx.x) * L::EPI + warp, int64_t(gridDim.x) * L::EPI, status);
     }
     tc_fence_before();
     __syncthreads();

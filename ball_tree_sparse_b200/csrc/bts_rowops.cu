@@ -31,11 +31,13 @@ __global__ void k_rotate_z(const float *__restrict__ in, int64_t n, float *__res
     }
 }
 
-__global__ void k_invert(const int32_t *__restrict__ perm, int64_t npad, int32_t *__restrict__ inv)
+__global__ void k_invert(const int32_t *__restrict__ perm, int64_t npad, int64_t n_rows, int32_t *__restrict__ inv,
+                         uint32_t *status)
 {
     for (int64_t s = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; s < npad; s += int64_t(gridDim.x) * blockDim.x) {
         const int32_t r = perm[s];
-        if (r >= 0) inv[r] = int32_t(s);
+        if (r >= n_rows) record_error(status, BT_ERR_INTERNAL);  // not a row: never write it
+        else if (r >= 0) inv[r] = int32_t(s);
     }
 }
 
@@ -109,7 +111,10 @@ extern "C" bt_status bt_invert_perm(const int32_t *perm, int64_t npad, int64_t n
 {
     if (!perm || !inv || npad < 0 || n_rows < 0 || n_rows > npad) return BT_ERR_ARG;
     if (npad == 0) return BT_OK;
-    k_invert<<<grid_for(npad, kRowThreads), kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(perm, npad, inv);
+    uint32_t *status = stream_status(static_cast<cudaStream_t>(stream));
+    if (!status) return BT_ERR_CUDA;
+    k_invert<<<grid_for(npad, kRowThreads), kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(perm, npad, n_rows, inv,
+                                                                                                status);
     return cudaPeekAtLastError() == cudaSuccess ? BT_OK : BT_ERR_CUDA;
 }
 

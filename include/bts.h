@@ -188,7 +188,8 @@ bt_status bt_rotate_z(const float *in, int64_t N, float *out, void *stream);
  *           0..n_rows-1 exactly once (as bt_build* produces)
  *   inv     int32 [n_rows] out
  * Only the entries of the rows that slots name are written.  Where some row may
- * have no slot, fill inv with BT_NO_SLOT first.
+ * have no slot, fill inv with BT_NO_SLOT first.  A perm entry >= n_rows is
+ * skipped and recorded as BT_ERR_INTERNAL.
  */
 bt_status bt_invert_perm(const int32_t *perm, int64_t npad, int64_t n_rows, int32_t *inv, void *stream);
 
@@ -259,7 +260,8 @@ bt_status bt_ball_attention(const void *Q, const void *K, const void *V, const i
  *            (the layout of a linear layer's weight)
  *   perm     int32 [npad] device (slot -> row, -1 dummy) or NULL.  Given
  *            perm, Q, K, V are [npad, H, d] in slot order and the rows of the
- *            dummy slots are set to zero; inv (int32 [rows] device, inv[r] =
+ *            dummy slots are set to zero (an entry >= rows is a dummy,
+ *            recorded as BT_ERR_INTERNAL); inv (int32 [rows] device, inv[r] =
  *            the slot of row r, as bt_invert_perm writes it) is required.  A
  *            row whose inv entry is BT_NO_SLOT is stored nowhere; any other
  *            entry outside [0, npad) is skipped and recorded as
