@@ -1007,11 +1007,10 @@ extern "C" bt_status bt_projected_ball_attention(const void *X, const int32_t *p
     uint8_t *w = static_cast<uint8_t *>(ws);
     void *Q = w, *K = w + one, *V = w + 2 * one;
     int32_t *inv = reinterpret_cast<int32_t *>(w + 3 * one);
-    if (perm && pair_shape(m, H, d, dt, rows) && npad >= 128) {
+    if (perm && pair_shape(m, H, d, dt, rows) && npad >= 128 && rows <= npad) {
         // Q, K, V written in slot order (each feature row to its slot); the attention then loads every ball as one
         // tile.  The workspace may hold another call's inverse: a row that no slot names must not be taken for one of
         // its slots.
-        if (rows > npad) return BT_ERR_ARG;
         if (cudaMemsetAsync(inv, 0x80, size_t(rows) * 4, static_cast<cudaStream_t>(stream)) != cudaSuccess)
             return BT_ERR_CUDA;
         bt_status s = bt_invert_perm(perm, npad, rows, inv, stream);
@@ -1020,7 +1019,7 @@ extern "C" bt_status bt_projected_ball_attention(const void *X, const int32_t *p
         if (s != BT_OK) return s;
         return bt_ball_attention_tree(Q, K, V, perm, npad, rows, m, H, d, dt, O, stream);
     }
-    // other shapes: Q, K, V in the original row order, then the gathering attention
+    // other shapes, and fewer slots than rows: Q, K, V in the original row order, then the gathering attention
     bt_status s = bt_qkv_project(X, rows, C, Wt, H, d, dt, nullptr, nullptr, 0, Q, K, V, stream);
     if (s != BT_OK) return s;
     return bt_ball_attention(Q, K, V, perm, npad, rows, m, H, d, dt, O, stream);

@@ -724,6 +724,7 @@ extern "C" bt_status bt_projected_ball_attention_i8(const void *X, const void *R
     if (reinterpret_cast<uintptr_t>(work) & 255u) return BT_ERR_ARG;
     // what the steps would refuse, before the first of them is enqueued
     if (int64_t(H) * d > 65535 / 3 || C > 65536) return BT_ERR_UNSUPPORTED;
+    if ((reinterpret_cast<uintptr_t>(ws) | reinterpret_cast<uintptr_t>(perm)) % 4) return BT_ERR_ARG;
     const LayerWs l(npad, rows, C, int64_t(H) * d, dt);
     uint8_t *p = static_cast<uint8_t *>(work);
     int8_t *xq = reinterpret_cast<int8_t *>(p);
@@ -732,8 +733,9 @@ extern "C" bt_status bt_projected_ball_attention_i8(const void *X, const void *R
     int32_t *inv = reinterpret_cast<int32_t *>(v + l.one);
     bt_status s = bt_rms_norm_i8(X, R, gamma, rows, C, eps, dt, Hout, xq, xs, stream);
     if (s != BT_OK || npad == 0) return s;
-    // the shapes of bt_ball_attention_tree: whole tiles in slot order; else the attention gathers rows
-    const bool tree = perm && dt == BT_BF16 && d == 32 && H % 2 == 0 && npad >= 128 && rows < 0x7FFFFFFF &&
+    // the shapes of bt_ball_attention_tree: whole tiles in slot order; else, and where slots are too few for the rows (an
+    // inverse has no more rows than slots), the attention gathers rows
+    const bool tree = perm && dt == BT_BF16 && d == 32 && H % 2 == 0 && npad >= 128 && rows <= npad && rows < 0x7FFFFFFF &&
                       (m == 16 || m == 32 || m == 64 || m == 128);
     if (tree) {
         // the workspace may hold another call's inverse: a row that no slot names must not be taken for one of its slots

@@ -295,10 +295,10 @@ bt_status bt_ball_attention_tree(const void *Qt, const void *Kt, const void *Vt,
 /*
  * One attention layer from the features [E7][E9]: bt_qkv_project into a
  * workspace, then ball attention.  For the shapes bt_ball_attention_tree takes
- * (and a non-NULL perm) the projections are written in slot order and the
- * attention loads whole tiles; otherwise they are written in the original
- * order and bt_ball_attention gathers them.  Arguments as for the two calls;
- * m and d as for bt_ball_attention.
+ * (and a non-NULL perm with rows <= npad) the projections are written in slot
+ * order and the attention loads whole tiles; otherwise they are written in the
+ * original order and bt_ball_attention gathers them.  Arguments as for the two
+ * calls; m and d as for bt_ball_attention.
  *   ws  workspace of bt_projected_workspace_size(npad, rows, H, d, dt) bytes,
  *       256-byte aligned (the projected Q, K and V, and the inverse of perm)
  * Rows that no slot names take no part, and their rows of O are left untouched.
