@@ -565,7 +565,9 @@ def _norm_inputs(X, weight, residual, hout):
 def bt_rms_norm(X: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
                 eps: float = 1e-6, out: torch.Tensor | None = None, hout: torch.Tensor | None = None, stream=None):
     """(Y, h): h = X + residual (X itself without one), Y = h * weight / sqrt(mean(h^2) + eps) by row.
-    X [rows, C] fp32 or bf16; weight float32 [C].  hout and out may be X or residual, but not one another."""
+    X [rows, C] fp32 or bf16; weight float32 [C].  hout and out may be X or residual, but not one another.  h is
+    None where out is X and there is no residual: Y has taken its place, and the backward pass needs a copy of X made
+    before."""
     rows, C, dt = _norm_inputs(X, weight, residual, hout)
     st = _handle(X.device, stream)
     if out is None:
@@ -577,7 +579,9 @@ def bt_rms_norm(X: torch.Tensor, weight: torch.Tensor | None = None, residual: t
         hout = _new(X, stream)
     _check("bt_rms_norm",
            _lib.bt_rms_norm(_at(X), _at(residual), _at(weight), rows, C, eps, dt, _at(hout), _at(out), st))
-    return out, (X if residual is None else hout)
+    if residual is not None:
+        return out, hout
+    return out, (None if rows and out.data_ptr() == X.data_ptr() else X)
 
 
 def _eight(X, out, scale, stream, others, same=()):
