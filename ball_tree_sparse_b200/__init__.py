@@ -476,6 +476,17 @@ def _new(like: torch.Tensor, stream, dtype=None):
     return torch.empty_like(like) if dtype is None else torch.empty_like(like, dtype=dtype)
 
 
+def _zeros(like: torch.Tensor, stream):
+    """_new, filled with zeros."""
+    with torch.cuda.stream(stream):
+        return torch.zeros_like(like)
+
+
+def _complete(perm, npad, rows):
+    """Whether the slots are enough to name every row, and all of perm's."""
+    return npad >= rows and (perm is None or npad == perm.numel())
+
+
 def _array(shape, dtype, device, stream):
     """The same of any shape (torch.empty_strided costs the host less than half of what torch.empty does)."""
     if stream is not None:
@@ -524,7 +535,8 @@ def bt_ball_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor
                                perm: torch.Tensor | None, m: int, out=None, npad: int | None = None, stream=None):
     """Gradients (dQ, dK, dV) of bt_ball_attention(Q, K, V, perm, m) for the gradient dO of its output; the
     probabilities are recomputed.  All tensors [rows, H, d], fp32 or bf16, original row order.  Rows that no slot
-    names are not written: give zeroed tensors as `out` where there are such rows."""
+    names are not written.  New results are zero there when there are fewer slots than rows or npad leaves out some of
+    perm's; otherwise perm is taken to name every row, as a tree does: where it does not, give zeroed tensors as `out`."""
     shape, dtype, dev = Q.shape, Q.dtype, Q.device
     rows, H, d = shape
     dt = _dt(Q)
@@ -534,7 +546,8 @@ def bt_ball_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor
     npad = _slots(perm, npad, rows, dev)
     st = _handle(dev, stream)
     if out is None:
-        dQ, dK, dV = _new(Q, stream), _new(Q, stream), _new(Q, stream)
+        make = _new if _complete(perm, npad, rows) else _zeros
+        dQ, dK, dV = make(Q, stream), make(Q, stream), make(Q, stream)
     else:
         dQ, dK, dV = out
         for n, t in (("dQ", dQ), ("dK", dK), ("dV", dV)):
@@ -724,7 +737,8 @@ def bt_projected_ball_attention_i8(X: torch.Tensor, perm: torch.Tensor | None, W
                                    work: torch.Tensor | None = None, npad: int | None = None, stream=None):
     """One pre-norm attention layer with an 8-bit projection: (O, h), with h = X + residual (X without one) and O
     the ball attention of Q/K/V projected from the normed rows in 8 bits.  X [rows, C]; Wq int8 [3*H*d, C] and ws
-    float32 [3*H*d] from bt_quantize_i8; O [rows, H, d] in X's type, original row order."""
+    float32 [3*H*d] from bt_quantize_i8; O [rows, H, d] in X's type, original row order.  Rows of O that no slot names
+    are as for bt_ball_attention_backward."""
     rows, C, dt = _norm_inputs(X, weight, residual, hout)
     dev = X.device
     _want("Wq", Wq, (3 * H * d, C), torch.int8, dev)
@@ -736,6 +750,9 @@ def bt_projected_ball_attention_i8(X: torch.Tensor, perm: torch.Tensor | None, W
         _apart("out", out, X, residual, weight, Wq, ws, perm, hout, work)
     else:
         out = _array((rows, H, d), X.dtype, dev, stream)
+        if not _complete(perm, npad, rows):
+            with torch.cuda.stream(stream):
+                out.zero_()
     if residual is not None and hout is None:
         hout = _new(X, stream)
     if work is None:
