@@ -700,10 +700,10 @@ def bt_qkv_project_i8(Xq: torch.Tensor, xs: torch.Tensor, Wq: torch.Tensor, ws: 
     st = _handle(dev, stream)
     if perm is None or npad == 0:
         inv = None
-    elif inv is None:
-        inv = _inverse(perm, rows, _array((rows,), torch.int32, dev, stream), stream)
-    else:
+    elif inv is not None:
         _want("inv", inv, (rows,), torch.int32, dev)
+    elif rows:
+        inv = _inverse(perm, rows, _array((rows,), torch.int32, dev, stream), stream)
     shape = (npad, H, d)
     if out is None:
         if H * d % 8 == 0:  # each aligned to 16 bytes
