@@ -115,6 +115,13 @@ def _dptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _temporary(n: int, dtype, device, stream) -> torch.Tensor:
+    """Memory that a call makes and gives back itself: it belongs to the stream that uses it, whose allocator hands it out
+    again in that stream's order."""
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
 def _offsets_array(offsets) -> np.ndarray:
     return np.ascontiguousarray(np.asarray(offsets, dtype=np.int64))
 
@@ -146,7 +153,8 @@ def bt_build(coords: torch.Tensor, m: int, perm: torch.Tensor | None = None, ws:
     if perm is None:
         perm = torch.empty(N, dtype=torch.int32, device=coords.device)
     if ws is None:
-        ws = workspace([0, N], m, coords.device)
+        with torch.cuda.stream(stream):
+            ws = workspace([0, N], m, coords.device)
     _check("bt_build", _lib.bt_build(_dptr(coords), N, m, _dptr(perm), _dptr(ws), ws.numel(), _stream(stream)))
     return perm
 
@@ -175,7 +183,8 @@ def _segmented(name, coords, offsets, m, perm, ws, stream, *flags):
         sizes = [_padded(int(off[b + 1] - off[b]), m) for b in range(B)]
         perm = torch.empty(sum(sizes), dtype=torch.int32, device=coords.device)
     if ws is None:
-        ws = workspace(off, m, coords.device)
+        with torch.cuda.stream(stream):
+            ws = workspace(off, m, coords.device)
     _check(name, getattr(_lib, name)(_dptr(coords), off.ctypes.data_as(_P), B, m, _dptr(perm),
                                      pad.ctypes.data_as(_P), _dptr(ws), ws.numel(), *flags, _stream(stream)))
     return perm, pad
@@ -328,7 +337,7 @@ def bt_coarse_ball_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, 
         n = bt_coarse_workspace_size(npad, H, d, stride, Q.dtype)
         if n == 0:
             raise BtsError("bt_coarse_workspace_size", 1)
-        ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
+        ws = _temporary(n, torch.uint8, Q.device, stream)
     _check("bt_coarse_ball_attention",
            _lib.bt_coarse_ball_attention(_dptr(Q), _dptr(K), _dptr(V), _dptr(perm), npad, rows, m, H, d, _dt(Q),
                                          stride, _dptr(out), _dptr(ws), ws.numel(), _stream(stream)))
@@ -343,7 +352,7 @@ def bt_qkv_project(X: torch.Tensor, Wt: torch.Tensor, H: int, d: int, perm: torc
     rows, C = X.shape
     npad = perm.numel() if perm is not None else rows
     if perm is not None and inv is None:
-        inv = _inverse(perm, rows, torch.empty(rows, dtype=torch.int32, device=perm.device), stream)
+        inv = _inverse(perm, rows, _temporary(rows, torch.int32, perm.device, stream), stream)
     if out is None:
         out = tuple(torch.empty((npad, H, d), dtype=X.dtype, device=X.device) for _ in range(3))
     Q, K, V = out
@@ -382,7 +391,7 @@ def bt_projected_ball_attention(X: torch.Tensor, perm: torch.Tensor | None, Wt: 
         n = bt_projected_workspace_size(npad, rows, H, d, X.dtype)
         if n == 0:
             raise BtsError("bt_projected_workspace_size", 1)
-        ws = torch.empty(n, dtype=torch.uint8, device=X.device)
+        ws = _temporary(n, torch.uint8, X.device, stream)
     _check("bt_projected_ball_attention",
            _lib.bt_projected_ball_attention(_dptr(X), _dptr(perm), npad, rows, C, _dptr(Wt), m, H, d, _dt(X),
                                             _dptr(out), _dptr(ws), ws.numel(), _stream(stream)))
@@ -421,7 +430,7 @@ def bsa_forward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, perm: torch.T
         n = bsa_workspace_size(npad, rows, m, H, d, topk)
         if n == 0:
             raise BtsError("bsa_workspace_size", 2)
-        ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
+        ws = _temporary(n, torch.uint8, Q.device, stream)
     _check("bsa_forward",
            _lib.bsa_forward(_dptr(Q), _dptr(K), _dptr(V), _dptr(perm), npad, rows, m, H, d, BT_BF16, _dptr(X),
                             X.shape[1], _dptr(Wg), _dptr(bg), bsa_params(topk, int(mask_own_ball), int(coarsen_queries)),
