@@ -2,8 +2,8 @@
 //
 //   out[o(r), j] = (sum_c Xq[r, c] Wq[j, c]) * xs[r] * ws[j],   o(r) = inv[r] (slot order) or r
 //
-// The sum is exact in 32-bit integers (C <= 65536 values of at most 128 * 128), so only the two scales and the
-// output's type round.
+// The sum is exact in 32-bit integers (C <= 65536 values of at most 128 * 128).  Its conversion to float rounds beyond
+// 2^24, each of the two scales rounds, and a 16-bit result rounds once more.
 //
 //  - k_project_i8_few   few rows: a warp per output channel, which reads the channel's weights once for up to
 //                       eight rows.  Bound by the weights' bytes and by latency.

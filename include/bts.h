@@ -42,7 +42,8 @@
  *  - Calls may come from several host threads: the per-device set-up on a
  *    device's first call is done once, under a lock inside the library.
  *    Workspaces (and bt_build_noalloc's static scratch) are not shared safely
- *    between builds in flight at the same time; that is the caller's to avoid.
+ *    between calls in flight at the same time, replays of captured ones
+ *    included; that is the caller's to avoid.
  */
 #ifndef BTS_H
 #define BTS_H
@@ -447,7 +448,9 @@ bt_status bt_ball_attention_backward(const void *Q, const void *K, const void *V
  *         (BT_ERR_ARG otherwise).  May be X or R itself.
  *   Y     dt [rows, C] out; may be X or R itself, but not Hout
  *   1 <= C <= 8192 (BT_ERR_UNSUPPORTED above);  eps >= 0 and finite
- * The sum of squares and the norm are in float.  rows = 0 is a no-op.
+ * The sum of squares and the norm are in float: a row whose squares add up to
+ * more than float holds (values of about 1e19) becomes zeros, and with eps = 0 a
+ * row whose squares add up to 0 becomes NaN or infinite.  rows = 0 is a no-op.
  */
 bt_status bt_rms_norm(const void *X, const void *R, const float *w, int64_t rows, int32_t C, float eps, bt_dtype dt,
                       void *Hout, void *Y, void *stream);
@@ -458,7 +461,8 @@ bt_status bt_rms_norm(const void *X, const void *R, const float *w, int64_t rows
  *     scale = max_c |y_c| / 127,   Yq = y / scale, rounded to nearest even
  * A row of zeros has scale 0; a row with a value that is not finite has scale
  * NaN (and Yq = 0), so that its products are NaN.
- *   Yq  int8 [rows, C] out;  scale  float [rows] out
+ *   Yq  int8 [rows, C] out;  scale  float [rows] out; neither may overlap
+ *       another tensor of the call
  */
 bt_status bt_rms_norm_i8(const void *X, const void *R, const float *w, int64_t rows, int32_t C, float eps, bt_dtype dt,
                          void *Hout, int8_t *Yq, float *scale, void *stream);
@@ -500,7 +504,11 @@ bt_status bt_rms_norm_backward(const void *dY, const void *dH, const void *Hs, c
  *   dt   type of Q, K and V
  *   perm, inv, npad, Q, K, V  as for bt_qkv_project (slot order with zero rows
  *        in the dummy slots, or the original order when perm is NULL)
- * The sum is exact (32-bit integers); the result is rounded to dt once.
+ * The sum is exact (32-bit integers).  It is converted to float (exactly up to
+ * 2^24), multiplied by xs[r] and then by ws[j] in float, and rounded to dt: at
+ * most three roundings of 2^-24 each for float results, and one of 2^-8 more
+ * for bf16.  Where sum * xs[r] leaves float's range the result does too,
+ * whatever ws[j] is.
  * C <= 65536, 3*H*d <= 65535 (BT_ERR_UNSUPPORTED).
  */
 bt_status bt_qkv_project_i8(const int8_t *Xq, const float *xs, int64_t rows, int32_t C, const int8_t *Wq,
