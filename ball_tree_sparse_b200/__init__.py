@@ -441,7 +441,8 @@ def bsa_forward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, perm: torch.T
 
 # ---------------------------------------------------------------------------
 # Training and 8-bit serving.  These calls check shapes, types and devices here; what they allocate (outputs and
-# workspaces not given) belongs to the stream the work is enqueued on.  A call's time on the host is what a small
+# workspaces not given) belongs to the stream the work is enqueued on.  Like the calls above they read and write memory
+# and build no autograd graph: gradients come from the backward calls.  A call's time on the host is what a small
 # problem costs, so the checks are kept to attribute comparisons.
 # ---------------------------------------------------------------------------
 # torch's own cheap look-ups of the current device and of its current stream's handle, where it has them
