@@ -61,9 +61,8 @@ __device__ __forceinline__ void zero_dummies(const int32_t *__restrict__ perm, i
     for (int64_t s0 = w * 32; s0 < npad; s0 += nw * 32) {
         const int64_t s = s0 + lane;
         const int32_t r = s < npad ? __ldg(perm + s) : 0;
-        const bool none = s < npad && r >= rows;
-        if (none) record_error(status, BT_ERR_INTERNAL);
-        uint32_t dead = __ballot_sync(0xffffffffu, r < 0 || none);
+        uint32_t dead = __ballot_sync(0xffffffffu, s < npad && uint32_t(r) >= uint32_t(rows));  // rows < 2^31
+        if (dead && r >= 0 && s < npad && r >= rows) record_error(status, BT_ERR_INTERNAL);
         while (dead) {
             const int64_t slot = s0 + __ffs(int(dead)) - 1;
             dead &= dead - 1;
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(I8Tile::THREADS, 1)
             if (row < rows) {
                 xr = __ldg(xs + row);
                 orow = inv ? __ldg(inv + row) : int32_t(row);
-                if (inv && (orow < 0 || orow >= npad)) {  // not a slot: never write it
+                if (uint32_t(orow) >= uint32_t(npad)) {  // not a slot: never write it (without inv, npad is rows)
                     if (orow != BT_NO_SLOT && quarter == 0 && chunk == 0) record_error(status, BT_ERR_INTERNAL);
                     orow = -1;
                 }
