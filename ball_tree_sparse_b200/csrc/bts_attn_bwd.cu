@@ -54,9 +54,10 @@ __device__ __forceinline__ bool finite4(const float4 &v)
 //   B  dV += P^T dO and dK += dS^T Q: a thread keeps KPT keys x 4 columns of each over all queries.
 //   C  dQ = dS K of the 32 queries.
 // Rows are padded by 16 bytes, which keeps the 16-byte accesses of A, B and C free of bank conflicts.
-// Bound by the float pipe and shared-memory loads together (A: 40 cycles of loads to 32 of products), and by latency, as
-// one to five CTAs fit an SM: 15 to 24 TFLOP/s (65,536 rows of 8 x 32 floats in balls of 128: 0.90 ms; 1.23 without the
-// bound on registers that lets two CTAs of that shape share an SM).
+// Bound by shared-memory loads (77% of their rate; A: 40 cycles of loads to 32 of products), and by latency, as one to five
+// CTAs fit an SM: 14 to 24 TFLOP/s.  65,536 rows of 8 x 32 floats in balls of 128: 0.90 ms, 73 us at the rate of a copy (1.23
+// ms without the bound on registers that lets two CTAs of that shape share an SM); in balls of 32 0.39 ms; bf16 in balls of 256
+// 1.92 ms, 36 us at the rate of a copy.
 // ---------------------------------------------------------------------------
 template <int D, int MP>
 struct BwdSimt {
@@ -320,10 +321,11 @@ __global__ void __launch_bounds__(BwdSimt<D, MP>::NT, D == 32 && MP == 128 ? 2 :
 // ball's own slots (`mend`).  One ball to a tile (m > 64) goes without those checks, and its dummies, rows of zeros, need a
 // mask in S alone: 85 us against 97 for the layer below.
 // Measured: 65,536 rows of 8 x 32 in balls of 128, 85 us (235 MB: 2.75 TB/s; 36 us at the rate of a copy); 1,048,576 rows
-// of 4 x 32, 604 to 630 us; 70,001 rows of 5 x 64 in balls of 64, 119 us.  Two things of about the same length bound it: the
-// gathers (58 cycles per request of four rows with two warps issuing: 7,400 of an item's 9,700 cycles for d = 32) and a
-// group's chain of waits and arithmetic (5,900 cycles from a tile's arrival to P and dS, 3,800 for the last products).
-// Without any loads the layer takes 80 us, without the exponentials 80.  The loops over keys are kept rolled: unrolled,
+// of 4 x 32, 604 to 630 us; 70,001 rows of 5 x 64 in balls of 64, 119 us.  A group's chain of waits and arithmetic bounds it:
+// 9,700 cycles for an item of d = 32 (5,900 from a tile's arrival to P and dS, 3,800 for the last products), with no unit
+// more than half busy; without any loads the layer still takes 80 us, and without the exponentials 80.  The gathers beside
+// it are not far behind (58 cycles per request of four rows with two warps issuing: 7,400 cycles), so that a shorter chain
+// would meet them next.  The loops over keys are kept rolled: unrolled,
 // the code did not fit the instruction cache, and its registers spilled (97 us).
 // ---------------------------------------------------------------------------
 template <int D>

@@ -15,7 +15,8 @@
 // same shape, so they share the shift.  Only where an address is not aligned is VEC 1.
 // Measured (bf16): 1,048,576 x 128 with residual 170 us, 98% of a copy's rate; 65,536 x 256 with residual 26 us (79%);
 // 1,048,576 x 128 with residual to 8 bits 176 us (83%: arithmetic); backward, 1,048,576 x 128 189 us (88%), 65,536 x 256
-// 32 us (64%); odd lengths are bound by the instructions for their edges (100,000 x 333: 115 us, 36%).
+// 32 us (64%), both with dH; odd lengths are bound by the instructions for their edges (100,000 x 333 with residual: 115 us,
+// 36%).
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -336,9 +337,9 @@ __global__ void __launch_bounds__(kNormThreads, NV * VEC == 32 && !SHIFT ? 3 : 0
 constexpr int kBwdBlocks = 148 * 4;  // rows of partial sums of dw, at most
 
 // Backward: whether the next row is loaded before a row is reduced, and blocks of 256 threads on an SM (what their registers
-// leave room for).  Floats: two vectors a thread, two blocks, the next row ahead (65,536 x 512: 94 us; one vector, no row
-// ahead, four blocks: 107).  16 bits have twice the arithmetic to a byte, and more threads do better than rows ahead
-// (65,536 x 1024: 123 us with one vector and four blocks; 143 with three and a row ahead).
+// leave room for).  Floats: two vectors a thread, two blocks, the next row ahead (65,536 x 512 with dH: 94 us; one vector, no
+// row ahead, four blocks: 107).  16 bits have twice the arithmetic to a byte, and more threads do better than rows ahead
+// (65,536 x 1024 with dH: 123 us with one vector and four blocks; 143 with three and a row ahead).
 template <typename T, int VEC, int NV>
 struct BwdShape {
     static constexpr bool AHEAD = sizeof(T) == 4 && NV <= 2 && VEC > 1;

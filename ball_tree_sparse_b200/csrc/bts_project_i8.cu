@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(256)
 // Bound by the integer products: 65,536 x 256 -> 768 keeps the tensor pipe active for 23 us (4,096 operations a cycle and
 // SM, half of what bf16 has); its 118 MB take 18 us.  Measured: 39 us; the rest is the launch, W's arrival, and eleven
 // tiles a CTA where 10.4 are due.  Eight storing warps instead of sixteen: 43.  Without TMA the copying warps bound it
-// (65,536 x 255: 114 us).
+// (65,536 x 255: 118 us, six times its bytes' 19; x 99: 77 us).
 // ---------------------------------------------------------------------------
 struct I8Tile {
     static constexpr int BM = 128, BK = 128, EPI = 16, THREADS = (EPI + 5) * 32;
